@@ -49,7 +49,7 @@ typedef enum {
     SK_ERR_CUDA = 5             /* a CUDA runtime call or launch failed */
 } sk_status;
 
-typedef enum { SK_BF16 = 0, SK_F32 = 1, SK_I8 = 2 } sk_dtype;
+typedef enum { SK_BF16 = 0, SK_F32 = 1, SK_I8 = 2, SK_I4 = 3 } sk_dtype;
 
 typedef enum { SK_LAYER_RING = 0, SK_LAYER_GLOBAL = 1 } sk_layer_kind;
 
@@ -102,10 +102,13 @@ typedef struct sk_rope_table sk_rope_table;
  *   k, v:    [batch][n_kv_heads][capacity][head_dim] of k_dtype / v_dtype
  *   k_scale: [batch][n_kv_heads][capacity] float, one scale per int8 K row (k_dtype
  *            SK_I8 only, else NULL)
+ *   4-bit caches (k_dtype = v_dtype = SK_I4): k holds the rows of K and V together,
+ *            [batch][n_kv_heads][capacity][SK_KV4_ROW_BYTES(head_dim)] bytes, and v is
+ *            NULL (see SK_KV4_ROW_BYTES).
  *   head, count: int32 [batch] (ring only; may be NULL for global layers)
  *   pos:     int64 [batch], tokens seen so far = the next absolute position
  *   err:     uint32 device error word, may be NULL
- * k_dtype in {SK_BF16, SK_F32, SK_I8}; v_dtype in {SK_BF16, SK_F32}.
+ * k_dtype in {SK_BF16, SK_F32, SK_I8}; v_dtype in {SK_BF16, SK_F32}; or both SK_I4.
  */
 typedef struct {
     int32_t kind;
@@ -149,8 +152,9 @@ typedef struct {
  * sink blocks, sinks = their token count gives them the role of the pinned sinks;
  * without, sinks = S keeps the request's own first S tokens (StreamingLLM on paged
  * memory).
- * k_dtype, v_dtype: SK_BF16 or SK_F32 (the same for both).  block_size a power of two
- * in [4, 1024].
+ * k_dtype, v_dtype: SK_BF16, SK_F32 or SK_I4 (the same for both).  A pool of SK_I4 holds
+ * K and V rows together in k_pool, [n_blocks][n_kv_heads][block_size][row bytes], and
+ * v_pool is NULL.  block_size a power of two in [4, 1024].
  */
 typedef struct {
     int32_t k_dtype;
@@ -171,6 +175,20 @@ typedef struct {
     int64_t* seq_lens;
     uint32_t* err;
 } sk_paged_layer;
+
+/*
+ * Bytes of a 4-bit cache row: one token of one kv head, K and V together, 5 bits a value
+ * (160 bytes at head_dim 128, where bf16 takes 512).  Each half of the row (K, then V) is
+ * head_dim / 2 bytes of codes, then one (m, s) pair of bf16, m first, per group of 32
+ * dims.  A dim stands for code * s + m, where over its group
+ *   m = the smallest value, rounded down to bf16,
+ *   s = (the largest value - m) / 15, rounded up to bf16,
+ *   code = rint((x - m) / s), half to even, in [0, 15] (0 where s = 0),
+ * so that a value is kept to within s / 2.  Codes are little-endian 32-bit words in the
+ * order [t = 0..3][group]; nibble n of word (t, group) is dim 32 group + 8 t + n.  A
+ * non-finite value makes its whole group non-finite, and no other.
+ */
+#define SK_KV4_ROW_BYTES(head_dim) ((head_dim) + (head_dim) / 4)
 
 /* ---- RoPE table (host float64 build, device float32 copy) ---------------------- */
 
@@ -275,7 +293,8 @@ SK_API sk_status sk_rope_apply(const sk_rope_table* table, void* x, int32_t dtyp
  *      given, q must be NULL, and head_dim must be 64 or 128.
  *   q: [batch][T][n_q_heads][head_dim] of io_dtype, device, may be NULL; rotated in place.
  *   k: [batch][T][n_kv_heads][head_dim] of io_dtype, device; rotated in place, then
- *      written to the cache (quantised per row for an int8 K cache).
+ *      written to the cache (quantised per row for an int8 K cache; per group of 32 dims,
+ *      from the values k is left with, for a 4-bit cache, and so is v).
  *   v: [batch][T][n_kv_heads][head_dim] of io_dtype, device; written as is.
  * Token t of sequence b has absolute position P = pos[b] + t: the same counter gives
  * the angle and the slot ([RoPE] "Where the positions come from").
@@ -287,7 +306,8 @@ SK_API sk_status sk_rope_apply(const sk_rope_table* table, void* x, int32_t dtyp
  * SK_DEVERR_CAPACITY.  pos[b] += T.  pos[b] + T > max_positions skips the sequence
  * and sets SK_DEVERR_POSITION_RANGE.
  * io_dtype: SK_BF16 or SK_F32.  Supported (io, k cache, v cache): (F32,F32,F32),
- * (BF16,BF16,BF16), (BF16,I8,BF16); others return SK_ERR_UNSUPPORTED.
+ * (BF16,BF16,BF16), (BF16,I8,BF16), (BF16,I4,I4), (F32,I4,I4); others return
+ * SK_ERR_UNSUPPORTED.
  * n_q_heads must be a multiple of n_kv_heads when q is given.
  * T = 0 checks the layer, launches nothing (the state stays as it is) and returns
  * SK_OK; q, k and v may then be NULL. */
@@ -319,7 +339,9 @@ SK_API size_t sk_decode_workspace_bytes(const sk_kv_layer* layer, int32_t n_q_he
  * Supported: io SK_F32 with an F32/F32 cache, io SK_BF16 with a BF16/BF16 cache, and io
  * SK_BF16 with an I8/BF16 cache (int8 K codes and one fp32 scale per row in k_scale, as
  * sk_kv_append and sk_kv_rerotate write them; head_dim 128): a key is code * scale.
- * n_q_heads / n_kv_heads in {1, 2, 4} for head_dim 128 and {1, 2, 4, 8} for 64. */
+ * n_q_heads / n_kv_heads in {1, 2, 4} for head_dim 128 and {1, 2, 4, 8} for 64.
+ * 4-bit caches (SK_I4): io SK_BF16 or SK_F32, head_dim 64 or 128, n_q_heads / n_kv_heads
+ * in {1, 2, 4, 8}; a key or value is the fp32 code * s + m (|q| < 2^116). */
 SK_API sk_status sk_decode_attention(const sk_kv_layer* layer, const void* q_rot, int32_t n_q_heads,
                                      int32_t io_dtype, const float* sink_logits, void* out,
                                      void* workspace, size_t ws_bytes, void* stream);
@@ -380,7 +402,8 @@ SK_API size_t sk_decode_step_workspace_bytes(const sk_kv_layer* layer, int32_t n
  * The state (head, count, pos) changes in the second kernel; until the call's work is
  * done on the stream nothing else may read or write this layer.
  * Supported: ring and global layers with io SK_BF16 and a BF16/BF16 cache, or io
- * SK_F32 and an F32/F32 cache (int8 K caches: sk_kv_append + sk_decode_attention);
+ * SK_F32 and an F32/F32 cache (int8 K and 4-bit caches: sk_kv_append +
+ * sk_decode_attention);
  * n_q_heads / n_kv_heads as sk_decode_attention. */
 SK_API sk_status sk_decode_step(const sk_rope_table* table, const sk_kv_layer* layer, const void* q,
                                 int32_t n_q_heads, const void* k, const void* v, int32_t io_dtype,
@@ -420,8 +443,9 @@ SK_API size_t sk_prefill_workspace_bytes(int32_t batch, int32_t T, int32_t n_kv_
  *   by T_k - T_q).  Without a prior, keys before p0 are not seen.  A ring prior must
  *   have the call's sinks and window (window > 0) and a count of
  *   min(window, p0 - min(sinks, p0)), as appends through this library leave it; a
- *   global prior needs p0 <= capacity (SK_ERR_CAPACITY otherwise).  K and V bf16, same
- *   batch, n_kv_heads and head_dim.
+ *   global prior needs p0 <= capacity (SK_ERR_CAPACITY otherwise).  K and V bf16, or a
+ *   4-bit cache (SK_I4: its values are rounded to bf16 on the way to the tensor cores);
+ *   same batch, n_kv_heads and head_dim.
  *   A device state that does not match p0 sets SK_DEVERR_STATE in *err; the result
  *   is then undefined, and every read stays inside the cache.
  *   workspace: device, >= sk_prefill_workspace_bytes(batch, T, n_kv_heads, head_dim,
@@ -482,6 +506,17 @@ SK_API size_t sk_paged_decode_workspace_bytes(const sk_paged_layer* layer, int32
 SK_API sk_status sk_paged_decode_attention(const sk_paged_layer* layer, const void* q_rot, int32_t n_q_heads,
                                            int32_t io_dtype, const float* sink_logits, void* out,
                                            void* workspace, size_t ws_bytes, void* stream);
+
+/* ---- 4-bit cache rows as values ----------------------------------------------------- */
+
+/* Write the values that n_rows 4-bit cache rows stand for: rows is device memory of
+ * n_rows * SK_KV4_ROW_BYTES(head_dim) bytes (the k buffer of an SK_I4 layer, a pool, or
+ * any run of their rows); k, v: [n_rows][head_dim] of out_dtype, device.  A value is the
+ * fp32 code * s + m, rounded once to out_dtype (SK_BF16 or SK_F32).  Pointers 16-byte
+ * aligned; head_dim 64 or 128.  n_rows = 0 launches nothing and returns SK_OK; the
+ * pointers may then be NULL. */
+SK_API sk_status sk_kv4_unpack(const void* rows, int64_t n_rows, int32_t head_dim, void* k, void* v,
+                               int32_t out_dtype, void* stream);
 
 /* ---- Local-position caches: turn the recent keys on a window slide ---------------- */
 

@@ -624,6 +624,78 @@ def paged_decode_attention(q_rot: np.ndarray, k_pool: np.ndarray, v_pool: np.nda
 
 
 # ---------------------------------------------------------------------------
+# 4-bit cache rows (the library's own format; no page gives one).
+# ---------------------------------------------------------------------------
+
+def _bf16_bits_toward(x: np.ndarray, up: bool) -> np.ndarray:
+    """bf16 bits (uint16) of float32 x rounded towards +inf (up) or -inf."""
+    b = np.asarray(x, dtype=np.float32).view(np.uint32).astype(np.uint64)
+    grow = (b < 0x80000000) if up else (b >= 0x80000000)   # magnitude grows when rounding away from zero
+    return ((b + np.where(grow, 0xFFFF, 0).astype(np.uint64)) >> np.uint64(16)).astype(np.uint16)
+
+
+def _bf16_value(bits: np.ndarray) -> np.ndarray:
+    return (bits.astype(np.uint32) << np.uint32(16)).view(np.float32)
+
+
+def kv4_quantise(x: np.ndarray):
+    """Finite x [..., D] -> codes uint8 [..., D/32, 32], m and s bits uint16 [..., D/32]: per
+    group of 32 dims m = min rounded down to bf16, s = (max - m) / 15 rounded up to bf16,
+    code = rint((x - m) / s) in [0, 15].  The format fixes the arithmetic as float32
+    (one rounding for each difference and quotient), so codes are compared exactly."""
+    g = np.asarray(x, dtype=np.float32).reshape(*x.shape[:-1], -1, 32)
+    mb = _bf16_bits_toward(g.min(-1), up=False)
+    m = _bf16_value(mb)[..., None]
+    sb = _bf16_bits_toward((g.max(-1, keepdims=True) - m)[..., 0] / np.float32(15), up=True)
+    s = _bf16_value(sb)[..., None]
+    codes = np.rint((g - m) / np.where(s > 0, s, np.float32(1)))
+    codes = np.where(s > 0, np.clip(codes, 0, 15), 0).astype(np.uint8)
+    return codes, mb, sb
+
+
+def kv4_values(codes: np.ndarray, mb: np.ndarray, sb: np.ndarray) -> np.ndarray:
+    """The values code * s + m in float64, [..., D]."""
+    m = _bf16_value(mb).astype(np.float64)[..., None]
+    s = _bf16_value(sb).astype(np.float64)[..., None]
+    v = codes.astype(np.float64) * s + m
+    return v.reshape(*v.shape[:-2], v.shape[-2] * 32)
+
+
+def kv4_pack(k: np.ndarray, v: np.ndarray) -> np.ndarray:
+    """k, v [..., D] -> rows as bytes uint8 [..., 5 D / 4]: K codes, K (m, s) pairs, V codes,
+    V pairs.  Nibble n of the 32-bit word (t, group), words in the order [t][group], is dim
+    32 group + 8 t + n."""
+    out = []
+    for x in (k, v):
+        codes, mb, sb = kv4_quantise(x)
+        lead, ng = codes.shape[:-2], codes.shape[-2]
+        words = np.zeros(lead + (4, ng), dtype=np.uint32)
+        for grp in range(ng):
+            for t in range(4):
+                for n in range(8):
+                    words[..., t, grp] |= codes[..., grp, 8 * t + n].astype(np.uint32) << np.uint32(4 * n)
+        out.append(words.reshape(*lead, 4 * ng).astype("<u4").view(np.uint8))
+        out.append(np.ascontiguousarray(np.stack([mb, sb], -1).reshape(*lead, 2 * ng)).astype("<u2").view(np.uint8))
+    return np.concatenate(out, -1)
+
+
+def kv4_unpack(rows: np.ndarray):
+    """Rows as bytes [..., 5 D / 4] -> K, V float64 [..., D]."""
+    D = rows.shape[-1] * 4 // 5
+    ng = D // 32
+    out = []
+    for o in (0, D // 2 + D // 8):
+        words = np.ascontiguousarray(rows[..., o:o + D // 2]).view("<u4").reshape(*rows.shape[:-1], 4, ng)
+        pairs = np.ascontiguousarray(rows[..., o + D // 2:o + D // 2 + D // 8]).view("<u2")
+        pairs = pairs.reshape(*rows.shape[:-1], ng, 2)
+        codes = np.zeros(rows.shape[:-1] + (ng, 32), dtype=np.uint8)
+        for dim in range(D):
+            codes[..., dim // 32, dim % 32] = (words[..., dim % 32 // 8, dim // 32] >> np.uint32(4 * (dim % 8))) & 15
+        out.append(kv4_values(codes, pairs[..., 0], pairs[..., 1]))
+    return out[0], out[1]
+
+
+# ---------------------------------------------------------------------------
 # O7. Dynamic factor policy.
 # ---------------------------------------------------------------------------
 

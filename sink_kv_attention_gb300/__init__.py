@@ -17,6 +17,7 @@ sk_prefill_attention   prefill_attention
 sk_kv_rerotate         kv_rerotate
 sk_kv_shift_recent     kv_shift_recent
 sk_paged_*             PagedLayer, paged_append, paged_decode_attention
+sk_kv4_unpack          kv4_unpack (+ kv4_row_bytes)
 """
 from __future__ import annotations
 
@@ -31,7 +32,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libsinkkv.so")
 
 SK_OK, SK_ERR_ARG, SK_ERR_CAPACITY, SK_ERR_POSITION_RANGE, SK_ERR_UNSUPPORTED, SK_ERR_CUDA = range(6)
-SK_BF16, SK_F32, SK_I8 = 0, 1, 2
+SK_BF16, SK_F32, SK_I8, SK_I4 = 0, 1, 2, 3
 SK_LAYER_RING, SK_LAYER_GLOBAL = 0, 1
 SK_DEVERR_POSITION_RANGE, SK_DEVERR_CAPACITY, SK_DEVERR_TIMEOUT, SK_DEVERR_BLOCK_TABLE = 1, 2, 4, 8
 SK_DEVERR_STATE = 16
@@ -129,6 +130,8 @@ _SIGNATURES = [
                                                  ctypes.c_size_t, ctypes.c_void_p]),
     ("sk_kv_shift_recent", ctypes.c_int, [ctypes.POINTER(KVLayerStruct), ctypes.c_int32, ctypes.c_void_p,
                                           ctypes.c_int32, ctypes.c_void_p]),
+    ("sk_kv4_unpack", ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p,
+                                     ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p]),
     ("sk_sync_check", ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
                                      ctypes.POINTER(ctypes.c_uint32)]),
     ("sk_status_str", ctypes.c_char_p, [ctypes.c_int]),
@@ -176,7 +179,19 @@ def _sk_dtype(dt: torch.dtype) -> int:
         return SK_F32
     if dt == torch.int8:
         return SK_I8
+    if dt == torch.uint8:
+        return SK_I4  # rows of 4-bit codes and their parameters
     raise TypeError(f"unsupported dtype {dt}")
+
+
+def kv4_row_bytes(head_dim: int) -> int:
+    """Bytes of a 4-bit cache row, K and V of one token and kv head (SK_KV4_ROW_BYTES)."""
+    return head_dim + head_dim // 4
+
+
+def _row_head_dim(k: torch.Tensor) -> int:
+    """head_dim of a cache buffer [..., row]: its last size, or that of 4-bit rows."""
+    return k.shape[-1] * 4 // 5 if k.dtype == torch.uint8 else k.shape[-1]
 
 
 def _need_contig(*ts):
@@ -319,11 +334,12 @@ class KVLayer:
 
     k, v: [batch, n_kv_heads, capacity, head_dim]; k_scale: [batch, n_kv_heads, capacity]
     float32 (int8 K only); head, count: int32 [batch] (ring); pos: int64 [batch];
-    err: uint32 word as int32 [1].
+    err: uint32 word as int32 [1].  A 4-bit cache: k is uint8 [batch, n_kv_heads,
+    capacity, kv4_row_bytes(head_dim)], rows of K and V together, and v is None.
     """
     kind: int
     k: torch.Tensor
-    v: torch.Tensor
+    v: Optional[torch.Tensor]
     pos: torch.Tensor
     sinks: int = 0
     window: int = 0
@@ -335,14 +351,22 @@ class KVLayer:
     @staticmethod
     def allocate(kind: int, batch: int, n_kv_heads: int, head_dim: int, *, sinks: int = 0,
                  window: int = 0, capacity: Optional[int] = None, k_dtype=torch.bfloat16,
-                 v_dtype=torch.bfloat16, device="cuda", with_v: bool = True) -> "KVLayer":
+                 v_dtype=torch.bfloat16, device="cuda", with_v: bool = True,
+                 bits: Optional[int] = None) -> "KVLayer":
         """with_v=False leaves V as a one-row placeholder, for callers (such as a
-        key rerotation) that never touch V."""
+        key rerotation) that never touch V.  bits=4: a 4-bit cache (k_dtype, v_dtype and
+        with_v do not apply)."""
+        if bits not in (None, 4):
+            raise ValueError("bits must be 4 (or None: a cache of k_dtype and v_dtype)")
         if kind == SK_LAYER_RING:
             capacity = sinks + window
         assert capacity is not None and capacity >= 1
-        k = torch.zeros(batch, n_kv_heads, capacity, head_dim, dtype=k_dtype, device=device)
-        v = (torch.zeros(batch, n_kv_heads, capacity, head_dim, dtype=v_dtype, device=device) if with_v
+        if bits == 4:
+            k_dtype, row = torch.uint8, kv4_row_bytes(head_dim)
+        else:
+            row = head_dim
+        k = torch.zeros(batch, n_kv_heads, capacity, row, dtype=k_dtype, device=device)
+        v = None if bits == 4 else (torch.zeros(batch, n_kv_heads, capacity, head_dim, dtype=v_dtype, device=device) if with_v
              else torch.zeros(1, 1, 1, head_dim, dtype=v_dtype, device=device))
         ks = (torch.ones(batch, n_kv_heads, capacity, dtype=torch.float32, device=device)
               if k_dtype == torch.int8 else None)
@@ -365,13 +389,14 @@ class KVLayer:
 
     @property
     def head_dim(self):
-        return self.k.shape[3]
+        return _row_head_dim(self.k)
 
     def struct(self) -> KVLayerStruct:
         _need_contig(self.k, self.v, self.k_scale, self.head, self.count, self.pos)
-        return KVLayerStruct(self.kind, _sk_dtype(self.k.dtype), _sk_dtype(self.v.dtype), self.batch,
+        kd = _sk_dtype(self.k.dtype)
+        return KVLayerStruct(self.kind, kd, kd if self.v is None else _sk_dtype(self.v.dtype), self.batch,
                              self.n_kv_heads, self.head_dim, self.sinks, self.window, self.capacity,
-                             self.k.data_ptr(), self.v.data_ptr(),
+                             self.k.data_ptr(), None if self.v is None else self.v.data_ptr(),
                              None if self.k_scale is None else self.k_scale.data_ptr(),
                              None if self.head is None else self.head.data_ptr(),
                              None if self.count is None else self.count.data_ptr(),
@@ -541,9 +566,10 @@ def kv_rerotate(layers: Sequence[KVLayer], table_from: RopeTable, table_to: Rope
 class PagedLayer:
     """A paged layer's caller-owned device buffers (sk_paged_layer): pools
     [n_blocks, H_kv, block_size, D], block_table int32 [B, max_blocks] (-1 = no block),
-    sink_block_ids int32 [n_sink_blocks], seq_lens int64 [B]."""
+    sink_block_ids int32 [n_sink_blocks], seq_lens int64 [B].  A 4-bit cache: k_pool is
+    uint8 [n_blocks, H_kv, block_size, kv4_row_bytes(D)] and v_pool is None."""
     k_pool: torch.Tensor
-    v_pool: torch.Tensor
+    v_pool: Optional[torch.Tensor]
     block_table: torch.Tensor
     sink_block_ids: Optional[torch.Tensor]
     seq_lens: torch.Tensor
@@ -554,11 +580,15 @@ class PagedLayer:
     @staticmethod
     def allocate(batch: int, n_kv_heads: int, head_dim: int, *, block_size: int, n_blocks: int, max_blocks: int,
                  sinks: int = 0, window: int = 0, n_sink_blocks: int = 0, dtype=torch.bfloat16,
-                 device="cuda") -> "PagedLayer":
-        z = dict(dtype=dtype, device=device)
+                 device="cuda", bits: Optional[int] = None) -> "PagedLayer":
+        """bits=4: a 4-bit cache (dtype does not apply)."""
+        if bits not in (None, 4):
+            raise ValueError("bits must be 4 (or None: a cache of dtype)")
+        z = dict(dtype=dtype if bits is None else torch.uint8, device=device)
+        row = head_dim if bits is None else kv4_row_bytes(head_dim)
         return PagedLayer(
-            k_pool=torch.zeros(n_blocks, n_kv_heads, block_size, head_dim, **z),
-            v_pool=torch.zeros(n_blocks, n_kv_heads, block_size, head_dim, **z),
+            k_pool=torch.zeros(n_blocks, n_kv_heads, block_size, row, **z),
+            v_pool=torch.zeros(n_blocks, n_kv_heads, block_size, row, **z) if bits is None else None,
             block_table=torch.full((batch, max_blocks), -1, dtype=torch.int32, device=device),
             sink_block_ids=(torch.arange(n_sink_blocks, dtype=torch.int32, device=device)
                             if n_sink_blocks > 0 else None),
@@ -579,10 +609,12 @@ class PagedLayer:
 
     def struct(self) -> PagedLayerStruct:
         n_sink = 0 if self.sink_block_ids is None else self.sink_block_ids.numel()
-        return PagedLayerStruct(_sk_dtype(self.k_pool.dtype), _sk_dtype(self.v_pool.dtype), self.batch,
-                                self.n_kv_heads, self.k_pool.shape[3], self.block_size, self.block_table.shape[1],
+        kd = _sk_dtype(self.k_pool.dtype)
+        return PagedLayerStruct(kd, kd if self.v_pool is None else _sk_dtype(self.v_pool.dtype), self.batch,
+                                self.n_kv_heads, _row_head_dim(self.k_pool), self.block_size,
+                                self.block_table.shape[1],
                                 n_sink, self.sinks, self.window, self.k_pool.shape[0], self.k_pool.data_ptr(),
-                                self.v_pool.data_ptr(), self.block_table.data_ptr(),
+                                None if self.v_pool is None else self.v_pool.data_ptr(), self.block_table.data_ptr(),
                                 None if self.sink_block_ids is None else self.sink_block_ids.data_ptr(),
                                 self.seq_lens.data_ptr(), self.err.data_ptr())
 
@@ -626,6 +658,23 @@ def paged_decode_attention(layer: PagedLayer, q_rot: torch.Tensor, out: Optional
                                             workspace.numel() * workspace.element_size(), _stream(stream)),
            "sk_paged_decode_attention")
     return out
+
+
+def kv4_unpack(rows: torch.Tensor, dtype=torch.bfloat16, stream=None):
+    """The values that 4-bit cache rows stand for (sk_kv4_unpack): rows uint8 [..., row bytes]
+    (a 4-bit KVLayer's k, a PagedLayer's k_pool, or any contiguous run of their rows) ->
+    K, V of dtype (bf16 or fp32) [..., head_dim]."""
+    if rows.dtype != torch.uint8:
+        raise TypeError("rows must be uint8")
+    _need_contig(rows)
+    D = _row_head_dim(rows)
+    if rows.shape[-1] != kv4_row_bytes(D):
+        raise ValueError("rows are not 4-bit cache rows")
+    K = torch.empty(*rows.shape[:-1], D, dtype=dtype, device=rows.device)
+    V = torch.empty_like(K)
+    _check(_lib().sk_kv4_unpack(_ptr(rows), rows.numel() // rows.shape[-1], D, _ptr(K), _ptr(V), _sk_dtype(dtype),
+                                _stream(stream)), "sk_kv4_unpack")
+    return K, V
 
 
 def kv_shift_recent(layers: Sequence[KVLayer], table: RopeTable, delta: int, stream=None):

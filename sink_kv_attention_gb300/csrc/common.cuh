@@ -280,16 +280,24 @@ namespace sk {
 // Kernel-side layer kind of a paged layer (sk_paged_layer); not an sk_layer_kind.
 constexpr int kKindPaged = 2;
 
+// K and V buffers of a layer: both given, or for 4-bit rows (K and V together) one
+// buffer in the place of K and none in the place of V.
+inline bool kv_buffers_ok(int k_dtype, int v_dtype, const void* k, const void* v) {
+    if (k_dtype == SK_I4 || v_dtype == SK_I4) return k_dtype == v_dtype && k != nullptr && v == nullptr;
+    return k != nullptr && v != nullptr;
+}
+
 // Host check of a paged layer descriptor shared by the paged entry points.
 inline sk_status paged_layer_check(const sk_paged_layer& L) {
-    if (L.k_pool == nullptr || L.v_pool == nullptr || L.block_table == nullptr || L.seq_lens == nullptr)
-        return SK_ERR_ARG;
+    if (!kv_buffers_ok(L.k_dtype, L.v_dtype, L.k_pool, L.v_pool)) return SK_ERR_ARG;
+    if (L.block_table == nullptr || L.seq_lens == nullptr) return SK_ERR_ARG;
     if (L.batch < 1 || L.n_kv_heads < 1 || L.max_blocks < 1 || L.n_blocks < 1) return SK_ERR_ARG;
     if (L.head_dim != 64 && L.head_dim != 128) return SK_ERR_ARG;
     if (L.block_size < 4 || L.block_size > 1024 || (L.block_size & (L.block_size - 1)) != 0) return SK_ERR_ARG;
     if (L.n_sink_blocks < 0 || (L.n_sink_blocks > 0 && L.sink_block_ids == nullptr)) return SK_ERR_ARG;
     if (int64_t(L.n_sink_blocks) * L.block_size > (int64_t(1) << 30)) return SK_ERR_ARG;
-    if (L.sinks < 0 || L.k_dtype != L.v_dtype || (L.k_dtype != SK_BF16 && L.k_dtype != SK_F32)) return SK_ERR_ARG;
+    if (L.sinks < 0 || L.k_dtype != L.v_dtype || (L.k_dtype != SK_BF16 && L.k_dtype != SK_F32 && L.k_dtype != SK_I4))
+        return SK_ERR_ARG;
     if ((reinterpret_cast<uintptr_t>(L.k_pool) | reinterpret_cast<uintptr_t>(L.v_pool)) & 15u) return SK_ERR_ARG;
     return SK_OK;
 }

@@ -1,7 +1,8 @@
 // Entry points of decode attention over contiguous and paged layers: argument checks,
 // dispatch over (dtype, head_dim, n_rep) and the launches.  The kernels are in
 // decode_kernels.cuh, shared with the decode step that folds the append in
-// (decode_step.cu).
+// (decode_step.cu); 4-bit caches have their own in decode4.cu.
+#include "decode4.cuh"
 #include "decode_kernels.cuh"
 
 namespace sk {
@@ -47,6 +48,15 @@ bool route(int io_dtype, const sk_kv_layer& L, int nrep, bool want_ws, DecodePar
     return false;
 }
 
+// A call over a 4-bit cache, ring, global or paged.
+sk_status run_kv4(const Kv4DecodeArgs& a, size_t need, size_t ws_bytes, void* stream) {
+    SK_RET_IF(need == 0 || (a.io_dtype != SK_BF16 && a.io_dtype != SK_F32), SK_ERR_UNSUPPORTED);
+    SK_RET_IF(ws_bytes < need, SK_ERR_ARG);
+    cudaError_t e = cudaSuccess;
+    if (!kv4_decode_run(a, static_cast<cudaStream_t>(stream), &e)) return SK_ERR_UNSUPPORTED;
+    return e == cudaSuccess ? SK_OK : SK_ERR_CUDA;
+}
+
 }  // namespace
 }  // namespace sk
 
@@ -57,6 +67,8 @@ extern "C" size_t sk_decode_workspace_bytes(const sk_kv_layer* layer, int32_t n_
     size_t ws = 0;
     cudaError_t e = cudaSuccess;
     const int nrep = n_q_heads / layer->n_kv_heads;
+    if (layer->k_dtype == SK_I4)
+        return kv4_decode_workspace(layer->batch, layer->n_kv_heads, layer->head_dim, nrep);
     const int io = layer->k_dtype == SK_F32 ? SK_F32 : SK_BF16;
     if (!route(io, *layer, nrep, true, nullptr, nullptr, &ws, &e)) return 0;
     return ws;
@@ -74,6 +86,9 @@ extern "C" sk_status sk_decode_attention(const sk_kv_layer* layer, const void* q
     const int nrep = n_q_heads / L.n_kv_heads;
     size_t need = 0;
     cudaError_t e = cudaSuccess;
+    if (L.k_dtype == SK_I4)
+        return run_kv4(Kv4DecodeArgs{layer, nullptr, q_rot, sink_logits, out, workspace, nrep, io_dtype},
+                       sk_decode_workspace_bytes(layer, n_q_heads), ws_bytes, stream);
     if (!route(io_dtype, L, nrep, true, nullptr, nullptr, &need, &e)) return SK_ERR_UNSUPPORTED;
     SK_RET_IF(ws_bytes < need, SK_ERR_ARG);
     DecodeParams p{};
@@ -127,6 +142,8 @@ sk_status check_paged(const sk_paged_layer* layer, int32_t n_q_heads) {
 
 extern "C" size_t sk_paged_decode_workspace_bytes(const sk_paged_layer* layer, int32_t n_q_heads) {
     if (check_paged(layer, n_q_heads) != SK_OK) return 0;
+    if (layer->k_dtype == SK_I4)
+        return kv4_decode_workspace(layer->batch, layer->n_kv_heads, layer->head_dim, n_q_heads / layer->n_kv_heads);
     const sk_kv_layer L = paged_as_layer(*layer);
     size_t ws = 0;
     cudaError_t e = cudaSuccess;
@@ -145,6 +162,9 @@ extern "C" sk_status sk_paged_decode_attention(const sk_paged_layer* layer, cons
     const sk_paged_layer& PL = *layer;
     const sk_kv_layer L = paged_as_layer(PL);
     const int nrep = n_q_heads / L.n_kv_heads;
+    if (PL.k_dtype == SK_I4)
+        return run_kv4(Kv4DecodeArgs{nullptr, layer, q_rot, sink_logits, out, workspace, nrep, io_dtype},
+                       sk_paged_decode_workspace_bytes(layer, n_q_heads), ws_bytes, stream);
     size_t need = 0;
     cudaError_t e = cudaSuccess;
     if (!route(io_dtype, L, nrep, true, nullptr, nullptr, &need, &e)) return SK_ERR_UNSUPPORTED;
@@ -214,7 +234,9 @@ extern "C" sk_status sk_decode_attention_noalloc(const sk_kv_layer* layer, const
     const int nrep = n_q_heads / layer->n_kv_heads;
     size_t need = 0;
     cudaError_t e = cudaSuccess;
-    if (!route(io_dtype, *layer, nrep, true, nullptr, nullptr, &need, &e)) return SK_ERR_UNSUPPORTED;
+    if (layer->k_dtype == SK_I4) need = sk_decode_workspace_bytes(layer, n_q_heads);
+    else if (!route(io_dtype, *layer, nrep, true, nullptr, nullptr, &need, &e)) return SK_ERR_UNSUPPORTED;
+    SK_RET_IF(need == 0, SK_ERR_UNSUPPORTED);
     SK_RET_IF(need > SK_DECODE_NOALLOC_SCRATCH_BYTES, SK_ERR_CAPACITY);
     void* scratch = nullptr;
     s = noalloc_scratch(&scratch);

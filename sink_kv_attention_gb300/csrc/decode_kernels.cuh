@@ -1579,7 +1579,7 @@ struct DecodeLaunch {
 sk_status check_layer(const sk_kv_layer* layer, int32_t n_q_heads) {
     SK_RET_IF(layer == nullptr, SK_ERR_ARG);
     const sk_kv_layer& L = *layer;
-    SK_RET_IF(L.k == nullptr || L.v == nullptr || L.pos == nullptr, SK_ERR_ARG);
+    SK_RET_IF(!kv_buffers_ok(L.k_dtype, L.v_dtype, L.k, L.v) || L.pos == nullptr, SK_ERR_ARG);
     SK_RET_IF(L.batch < 1 || L.n_kv_heads < 1 || L.capacity < 1, SK_ERR_ARG);
     SK_RET_IF(L.batch > kMaxBatch, SK_ERR_UNSUPPORTED);
     SK_RET_IF(n_q_heads < 1 || n_q_heads % L.n_kv_heads != 0, SK_ERR_ARG);

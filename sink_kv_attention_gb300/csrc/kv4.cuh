@@ -1,0 +1,85 @@
+// The rows of a 4-bit KV cache, shared by the append, the attention and the unpacking.
+//
+// A row holds one token of one kv head, K and V together, so that a tile of a cache (or
+// a block of a pool) is one contiguous copy.  Each half (K, then V) is head_dim 4-bit
+// codes followed by one (m, s) pair of bf16 per group of 32 dims; dim i of the half
+// stands for code_i * s + m with
+//     m = the group's smallest value, rounded down to bf16
+//     s = (the group's largest value - m) / 15, rounded up to bf16
+//     code = rint((x - m) / s), half to even, in [0, 15]   (0 where s = 0)
+// so that |x - (code s + m)| <= s / 2 up to fp32 rounding.  m is exact when x is bf16.
+// A non-finite x makes m or s, and with them the whole group's values, non-finite.
+//
+// Codes are 32-bit words w[t][grp] (t = 0..3, grp = 0..head_dim/32-1): nibble n of the
+// word is dim 32 grp + 8 t + n.  A lane that owns word column t of a row so reads the
+// codes of every group with one load, and the even / odd nibbles of a word's low and
+// (shifted) high halves are, as they stand, fp16 subnormals (code * 2^-24, code * 2^-20).
+#pragma once
+
+#include "common.cuh"
+
+namespace sk {
+
+struct Kv4 {};  // tag: a cache of 4-bit rows
+
+constexpr int kv4_row_bytes(int D) { return D + D / 4; }    // K and V
+constexpr int kv4_half_bytes(int D) { return D / 2 + D / 8; }
+constexpr int kv4_word_offset(int D, int t, int grp) { return t * (D / 8) + grp * 4; }
+constexpr int kv4_param_offset(int D, int grp) { return D / 2 + grp * 4; }
+
+// Largest bf16 value <= x, smallest bf16 value >= x (x >= 0), as floats.
+__device__ __forceinline__ float bf16_floor(float x) {
+    const uint32_t b = __float_as_uint(x);
+    return __uint_as_float((int32_t(b) >= 0 ? b : b + 0xFFFFu) & 0xFFFF0000u);
+}
+
+__device__ __forceinline__ float bf16_ceil_nonneg(float x) {
+    return x != x ? x : __uint_as_float((__float_as_uint(x) + 0xFFFFu) & 0xFFFF0000u);
+}
+
+// Extremes that keep a NaN (fminf / fmaxf drop it, and a group would hide it).
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float y;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+
+// (m, s) of a group with extremes lo and hi.
+__device__ __forceinline__ void kv4_group_params(float lo, float hi, float* m, float* s) {
+    *m = bf16_floor(lo);
+    *s = bf16_ceil_nonneg(__fdiv_rn(hi - *m, 15.0f));
+}
+
+// The pair as stored: m in the low half of the word, s in the high half.
+__device__ __forceinline__ uint32_t kv4_param_word(float m, float s) {
+    return (__float_as_uint(m) >> 16) | (__float_as_uint(s) & 0xFFFF0000u);
+}
+
+__device__ __forceinline__ uint32_t kv4_code(float x, float m, float s) {
+    const float r = rintf(__fdiv_rn(x - m, s));       // NaN where s is 0 or not finite
+    return uint32_t(fminf(fmaxf(r, 0.0f), 15.0f));    // NaN -> 0
+}
+
+// Codes of n <= 8 values as nibbles 0 .. n - 1.
+template <int N>
+__device__ __forceinline__ uint32_t kv4_codes(const float* x, float m, float s) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) w |= kv4_code(x[i], m, s) << (4 * i);
+    return w;
+}
+
+// The 8 values of a word.
+__device__ __forceinline__ void kv4_decode_word(uint32_t w, uint32_t param, float* f) {
+    const float m = __uint_as_float(param << 16), s = __uint_as_float(param & 0xFFFF0000u);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = fmaf(float((w >> (4 * i)) & 15u), s, m);
+}
+
+}  // namespace sk

@@ -39,6 +39,7 @@
 #include <algorithm>
 #include <mutex>
 
+#include "kv4.cuh"
 #include "tcgen05.cuh"
 
 namespace sk {
@@ -528,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 // ring at position p0 holds ring_count = min(W, p0 - s0) entries; the chunk needs
 // the newest cr <= ring_count of them.
 struct PriorView {
-    const __nv_bfloat16* k;  // [B][Hkv][cap][HD]
+    const __nv_bfloat16* k;  // [B][Hkv][cap][HD]; 4-bit rows [B][Hkv][cap][row bytes] for a 4-bit cache
     const __nv_bfloat16* v;
     const int32_t* head;
     const int32_t* count;
@@ -557,6 +558,8 @@ __device__ __forceinline__ int64_t prior_slot(const PriorView& pv, int b, int j)
 // per 16 bytes of a K row and the same 16 bytes of its V row.  The thread of (b, j = 0,
 // g = 0, c = 0) checks that the prior's state matches the chunk's start (pos = p0; a ring
 // holds ring_count recent entries).
+// KV4: the prior holds 4-bit rows; a thread decodes one word of 8 codes of each.
+template <bool KV4>
 __global__ void __launch_bounds__(256) gather_prior_kernel(PriorView pv, __nv_bfloat16* __restrict__ kc,
                                                            __nv_bfloat16* __restrict__ vc, int B, int qpad, int Hkv,
                                                            uint32_t* err) {
@@ -571,13 +574,25 @@ __global__ void __launch_bounds__(256) gather_prior_kernel(PriorView pv, __nv_bf
         const int j = int(bj % qpad), b = int(bj / qpad);
         const int64_t dst = (bj * Hkv + g) * HD;
         if (j < qoff) {
-            const int64_t row = ((int64_t(b) * Hkv + g) * pv.cap + prior_slot(pv, b, j)) * HD;
+            const int64_t crow = (int64_t(b) * Hkv + g) * pv.cap + prior_slot(pv, b, j);
             if (j == 0 && g == 0 && c == 0) {
                 const bool ok = pv.pos[b] == pv.p0 && (pv.kind == SK_LAYER_GLOBAL || pv.count[b] == pv.ring_count);
                 if (!ok) set_error(err, SK_DEVERR_STATE);
             }
-            reinterpret_cast<uint4*>(kc + dst)[c] = reinterpret_cast<const uint4*>(pv.k + row)[c];
-            reinterpret_cast<uint4*>(vc + dst)[c] = reinterpret_cast<const uint4*>(pv.v + row)[c];
+            if constexpr (KV4) {
+                const uint8_t* half = reinterpret_cast<const uint8_t*>(pv.k) + crow * kv4_row_bytes(HD);
+                const int word = kv4_word_offset(HD, c % 4, c / 4), par = kv4_param_offset(HD, c / 4);
+#pragma unroll
+                for (int h = 0; h < 2; ++h, half += kv4_half_bytes(HD)) {
+                    float f[8];
+                    kv4_decode_word(*reinterpret_cast<const uint32_t*>(half + word),
+                                    *reinterpret_cast<const uint32_t*>(half + par), f);
+                    reinterpret_cast<uint4*>((h == 0 ? kc : vc) + dst)[c] = ElemIO<__nv_bfloat16>::pack(f);
+                }
+            } else {
+                reinterpret_cast<uint4*>(kc + dst)[c] = reinterpret_cast<const uint4*>(pv.k + crow * HD)[c];
+                reinterpret_cast<uint4*>(vc + dst)[c] = reinterpret_cast<const uint4*>(pv.v + crow * HD)[c];
+            }
         } else {
             reinterpret_cast<uint4*>(kc + dst)[c] = make_uint4(0, 0, 0, 0);
             reinterpret_cast<uint4*>(vc + dst)[c] = make_uint4(0, 0, 0, 0);
@@ -674,8 +689,8 @@ static sk_status prefill_launch(const void* q_rot, const void* k_rot, const void
     int64_t qoff = 0;
     if (prior != nullptr) {
         const sk_kv_layer& L = *prior;
-        SK_RET_IF(L.k == nullptr || L.v == nullptr || L.pos == nullptr, SK_ERR_ARG);
-        SK_RET_IF(L.k_dtype != SK_BF16 || L.v_dtype != SK_BF16, SK_ERR_UNSUPPORTED);
+        SK_RET_IF(!kv_buffers_ok(L.k_dtype, L.v_dtype, L.k, L.v) || L.pos == nullptr, SK_ERR_ARG);
+        SK_RET_IF(L.k_dtype != SK_I4 && (L.k_dtype != SK_BF16 || L.v_dtype != SK_BF16), SK_ERR_UNSUPPORTED);
         SK_RET_IF(L.batch != batch || L.n_kv_heads != n_kv_heads || L.head_dim != head_dim, SK_ERR_ARG);
         SK_RET_IF((reinterpret_cast<uintptr_t>(L.k) | reinterpret_cast<uintptr_t>(L.v)) & 15u, SK_ERR_ARG);
         int64_t s0 = 0, cr = 0;
@@ -739,7 +754,8 @@ static sk_status prefill_launch(const void* q_rot, const void* k_rot, const void
         SK_RET_IF(!make_map(&mv, vc, 4, dims, strides, kv_box), SK_ERR_CUDA);
         const int64_t threads = int64_t(batch) * qpad * n_kv_heads * (HD / 8);
         const int64_t blocks = std::min<int64_t>((threads + 255) / 256, int64_t(device_sm_count()) * 16);
-        gather_prior_kernel<<<unsigned(blocks), 256, 0, st>>>(pv, kc, vc, batch, int(qpad), n_kv_heads, err);
+        auto gather = prior->k_dtype == SK_I4 ? gather_prior_kernel<true> : gather_prior_kernel<false>;
+        gather<<<unsigned(blocks), 256, 0, st>>>(pv, kc, vc, batch, int(qpad), n_kv_heads, err);
         SK_CUDA_RET(cudaGetLastError());
     } else {
         mk = mkc;  // no prior: every key tile is the chunk's

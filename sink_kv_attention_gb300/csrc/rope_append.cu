@@ -10,6 +10,9 @@
 // LPR = head_dim / (16 bytes / element size) lanes, each holding one 16-byte vector,
 // so every load and store is a coalesced 16-byte access.  A NeoX pair (j, j + r/2)
 // lives in two lanes of the same row; the partner's vector arrives by shuffle.
+#include <type_traits>
+
+#include "kv4.cuh"
 #include "rope_lane.cuh"
 
 namespace sk {
@@ -209,6 +212,37 @@ template <> struct CacheStore<__nv_bfloat16> {
     }
 };
 
+// This lane's part of a 4-bit row half: x holds dims c VEC .. c VEC + VEC - 1 of the row
+// (c = lane within the row), `half` points at the half's bytes.  The lanes of a group of
+// 32 dims find its extremes by shuffle (every lane of the warp must call this), each
+// quantises its own values, and one word of 8 codes is stored per 8 dims: by each lane
+// for bf16 rows, by the even lane of a pair for fp32 rows.
+template <typename IO, int D>
+__device__ __forceinline__ void kv4_store(uint8_t* half, const float* x, int c, bool store) {
+    constexpr int VEC = RowLayout<IO, D>::VEC;
+    constexpr int LPG = 32 / VEC;  // lanes per group
+    float lo = x[0], hi = x[0];
+#pragma unroll
+    for (int i = 1; i < VEC; ++i) {
+        lo = min_nan(lo, x[i]);
+        hi = max_nan(hi, x[i]);
+    }
+#pragma unroll
+    for (int o = LPG / 2; o > 0; o >>= 1) {
+        lo = min_nan(lo, __shfl_xor_sync(kFull, lo, o));
+        hi = max_nan(hi, __shfl_xor_sync(kFull, hi, o));
+    }
+    float m, s;
+    kv4_group_params(lo, hi, &m, &s);
+    uint32_t w = kv4_codes<VEC>(x, m, s);
+    if constexpr (VEC == 4) w |= __shfl_xor_sync(kFull, w, 1) << 16;
+    const int grp = c / LPG, t = c % LPG * VEC / 8;
+    if (store) {
+        if (VEC == 8 || c % 2 == 0) *reinterpret_cast<uint32_t*>(half + kv4_word_offset(D, t, grp)) = w;
+        if (c % LPG == 0) *reinterpret_cast<uint32_t*>(half + kv4_param_offset(D, grp)) = kv4_param_word(m, s);
+    }
+}
+
 constexpr int kAppendStages = 4;  // tokens in flight per block
 
 // Shared memory of the append kernel: kAppendStages stages of one token's q, k and v
@@ -346,7 +380,13 @@ __global__ void __launch_bounds__(kThreads + 32) kv_append_kernel(AppendParams p
                 if (live && which == 1) reinterpret_cast<uint4*>(ktok + h * D)[c] = out;
                 const int64_t crow = crw.base + int64_t(h) * crw.hstride;  // cache row index
                 const bool store_kv = live && which != 0 && crw.ok;
-                if constexpr (sizeof(KC) == 1) {
+                if constexpr (std::is_same<KC, Kv4>::value) {
+                    // 4-bit rows: the key as it was left in k, the value as given
+                    ElemIO<IO>::unpack(out, f);
+                    uint8_t* half = static_cast<uint8_t*>(p.kc) + crow * kv4_row_bytes(D) +
+                                    (which == 2 ? kv4_half_bytes(D) : 0);
+                    kv4_store<IO, D>(half, f, c, store_kv);
+                } else if constexpr (sizeof(KC) == 1) {
                     // int8 K: symmetric absmax over the row, codes rint(x * 127 / max|x|), ties to even.
                     float amax = 0.0f;
 #pragma unroll
@@ -370,7 +410,9 @@ __global__ void __launch_bounds__(kThreads + 32) kv_append_kernel(AppendParams p
                     if (store_kv && which == 1)
                         reinterpret_cast<uint4*>(static_cast<KC*>(p.kc) + crow * D)[c] = out;
                 }
-                if (store_kv && which == 2) reinterpret_cast<uint4*>(static_cast<VC*>(p.vc) + crow * D)[c] = raw;
+                if constexpr (!std::is_same<KC, Kv4>::value) {
+                    if (store_kv && which == 2) reinterpret_cast<uint4*>(static_cast<VC*>(p.vc) + crow * D)[c] = raw;
+                }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty_bar[st]);
@@ -427,7 +469,7 @@ template <typename IO, typename KC, typename VC>
 cudaError_t dispatch_append(const AppendParams& p, int D, bool neox, cudaStream_t st) {
     // paged layers get their own instantiation, so the ring/global kernel keeps its
     // register budget (two blocks per SM)
-    if constexpr (sizeof(KC) != 1) {
+    if constexpr (!std::is_same<KC, int8_t>::value) {
         if (p.kind == kKindPaged) {
             if (D == 64)
                 return neox ? launch_append<IO, KC, VC, 64, true, true>(p, st)
@@ -486,6 +528,10 @@ sk_status run_append(const AppendParams& p, const sk_rope_config& c, int io_dtyp
         e = dispatch_append<float, float, float>(p, head_dim, neox, st);
     else if (io_dtype == SK_BF16 && k_dtype == SK_BF16 && v_dtype == SK_BF16)
         e = dispatch_append<__nv_bfloat16, __nv_bfloat16, __nv_bfloat16>(p, head_dim, neox, st);
+    else if (io_dtype == SK_BF16 && k_dtype == SK_I4 && v_dtype == SK_I4)
+        e = dispatch_append<__nv_bfloat16, Kv4, Kv4>(p, head_dim, neox, st);
+    else if (io_dtype == SK_F32 && k_dtype == SK_I4 && v_dtype == SK_I4)
+        e = dispatch_append<float, Kv4, Kv4>(p, head_dim, neox, st);
     else if (io_dtype == SK_BF16 && k_dtype == SK_I8 && v_dtype == SK_BF16 && p.kind != kKindPaged)
         e = dispatch_append<__nv_bfloat16, int8_t, __nv_bfloat16>(p, head_dim, neox, st);
     else
@@ -514,7 +560,7 @@ extern "C" sk_status sk_kv_append(const sk_rope_table* table, const sk_kv_layer*
         c.neox = 1;
         c.max_positions = int64_t(1) << 62;
     }
-    SK_RET_IF(L.k == nullptr || L.v == nullptr || L.pos == nullptr, SK_ERR_ARG);
+    SK_RET_IF(!kv_buffers_ok(L.k_dtype, L.v_dtype, L.k, L.v) || L.pos == nullptr, SK_ERR_ARG);
     SK_RET_IF(L.batch < 1 || L.n_kv_heads < 1 || T < 0, SK_ERR_ARG);
     SK_RET_IF(L.head_dim != c.head_dim, SK_ERR_ARG);
     if (L.kind == SK_LAYER_RING) {
