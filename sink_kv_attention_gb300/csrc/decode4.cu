@@ -49,27 +49,34 @@
 namespace sk {
 namespace {
 
-constexpr int kTileRows = 32;
 constexpr float kRefNone = -1e30f;  // reference of a head that has seen no key
 constexpr int kHead = 6;            // log2 of the weight at the reference, V scale 1
 constexpr float kSlack = 8.0f;      // a score may pass the reference by this much
 constexpr int kExpFloor = -60;      // V scales below 2^-60 are taken as 2^-60 in the reference
 constexpr uint32_t kLowNibbles = 0x000F000Fu, kHighNibbles = 0x00F000F0u;
 
-template <int D, int NREP> struct Cfg4 {
+// KVH kv heads share a block's unit: their q heads are columns 4 kv .. 4 kv + NREP - 1 of
+// the N side (KVH = 2, NREP <= 4) or 0 .. NREP - 1 (KVH = 1).
+template <int D, int NREP, int KVH> struct Cfg4 {
     static constexpr int NG = D / 32;                      // groups
     static constexpr int ROWB = kv4_row_bytes(D);
-    static constexpr int NWARPS = NREP == 8 ? 8 : 12;
-    static constexpr int SLOTS = NREP == 8 ? 4 : 3;
-    static constexpr int SLOT_BYTES = kTileRows * ROWB;
-    static constexpr int MERGE_FLOATS = NREP * (D + 2);    // per warp
-    static constexpr size_t OFF_ZERO = size_t(NWARPS) * SLOTS * SLOT_BYTES;  // a row of zeros
-    static constexpr size_t OFF_MERGE = OFF_ZERO + (ROWB + 15) / 16 * 16;
-    static constexpr size_t OFF_PRE = OFF_MERGE + size_t(NWARPS) * MERGE_FLOATS * 4;
+    static constexpr int HEADS = NREP * KVH;               // q heads of a unit
+    static constexpr int TR = 32 / KVH;                    // rows of a tile (of each kv head)
+    static constexpr int NWARPS = HEADS == 8 && KVH == 1 ? 8 : 12;
+    static constexpr int HEAD_BYTES = TR * ROWB;           // a kv head's rows in a slot
+    static constexpr int SLOT_BYTES = KVH * HEAD_BYTES;
+    static constexpr int MERGE_FLOATS = HEADS * (D + 2);   // per warp
+    // half of the warps' states at a time where all of them would not leave room for 3 slots
+    static constexpr int MERGE_ROUNDS = NWARPS * MERGE_FLOATS * 4 > 36 * 1024 ? 2 : 1;
+    static constexpr int MERGE_WARPS = NWARPS / MERGE_ROUNDS;
+    static constexpr int SLOTS = NWARPS == 8 ? 4 : 3;
+    static constexpr size_t OFF_MERGE = size_t(NWARPS) * SLOTS * SLOT_BYTES;
+    static constexpr size_t OFF_PRE = OFF_MERGE + size_t(MERGE_WARPS) * MERGE_FLOATS * 4;
     static constexpr size_t OFF_BAR = OFF_PRE + (kMaxBatch + 1) * 8;
     static constexpr size_t SMEM = OFF_BAR + NWARPS * SLOTS * 8;
     static constexpr int THREADS = NWARPS * 32;
-    static constexpr int PARTIAL_FLOATS = NREP * (D + 2);
+    static constexpr int PARTIAL_FLOATS = HEADS * (D + 2);
+    static_assert(KVH == 1 || (KVH == 2 && NREP <= 4), "columns");
     static_assert(OFF_PRE % 8 == 0 && SMEM <= 232448, "shared memory");
 };
 
@@ -81,6 +88,16 @@ __device__ __forceinline__ void mma16816(float* c, uint32_t a0, uint32_t a1, uin
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The same with a zero C.
+__device__ __forceinline__ void mma16816_first(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 // An 8 x 8 matrix of 16-bit values, one row per 4 lanes, transposed within the warp.
@@ -99,6 +116,11 @@ __device__ __forceinline__ float2 half2_floats(uint32_t w) {
     return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
+__device__ __forceinline__ uint32_t half2_times(uint32_t w, __half2 f) {
+    const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&w), f);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
 __device__ __forceinline__ float pow2f(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }  // normal range
 
 template <int NG> __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
@@ -113,7 +135,7 @@ template <int NG> __device__ __forceinline__ void load_words(const uint8_t* p, u
 
 // The tiles of a block's share that fall to one warp, in order: tile i of the share
 // (counted over all its units) goes to warp i % NWARPS.
-template <int NWARPS>
+template <int NWARPS, int TR>
 struct TileWalk {
     UnitWalk w;
     int64_t lo, hi, cap;   // the share; rows a unit may hold
@@ -123,7 +145,7 @@ struct TileWalk {
         const int64_t st = w.start();
         r0 = max(lo, st) - st;
         r1 = min(min(hi, st + w.len()) - st, cap);
-        nt = r1 > r0 ? int((r1 - r0 + kTileRows - 1) / kTileRows) : 0;
+        nt = r1 > r0 ? int((r1 - r0 + TR - 1) / TR) : 0;
         k = (warp + NWARPS - gt0 % NWARPS) % NWARPS;
     }
     __device__ __forceinline__ void begin(const int64_t* pre, int B, int Hkv, int64_t lo_, int64_t hi_, int64_t cap_,
@@ -149,32 +171,37 @@ struct TileWalk {
             if (!next_unit(warp)) return false;
         return true;
     }
-    __device__ __forceinline__ int64_t row() const { return r0 + int64_t(k) * kTileRows; }
-    __device__ __forceinline__ int rows() const { return int(min(int64_t(kTileRows), r1 - row())); }
+    __device__ __forceinline__ int64_t row() const { return r0 + int64_t(k) * TR; }
+    __device__ __forceinline__ int rows() const { return int(min(int64_t(TR), r1 - row())); }
 };
 
-// Fills `slot` with the walk's tile (the whole warp).  Contiguous: one copy.  Paged: lane
-// i finds the pool row of the tile's row i; the first row of each run of consecutive pool
+// Fills `slot` with the walk's tile (the whole warp): the rows of each kv head of the
+// unit, one after the other.  Contiguous: one copy per kv head.  Paged: lane kv TR + i
+// finds the pool row of the tile's row i; the first row of each run of consecutive pool
 // rows copies the run.
-template <typename C, bool PAGED, typename Walk>
+template <typename C, int KVH, bool PAGED, typename Walk>
 __device__ __forceinline__ void load_tile(const DecodeParams& p, const Walk& t, uint8_t* slot, uint64_t* bar,
                                           uint64_t policy, int lane, bool* bad) {
     const int n = t.rows();
-    const int b = t.w.b, g = t.w.g;
+    const int b = t.w.b, g = t.w.g * KVH, heads = p.Hkv * KVH;
     const uint8_t* rows = static_cast<const uint8_t*>(p.kc);
     if constexpr (!PAGED) {
         if (lane == 0) {
-            mbar_arrive_expect_tx(bar, uint32_t(n) * C::ROWB);
-            bulk_copy_g2s(slot, rows + ((int64_t(b) * p.Hkv + g) * p.cap + t.row()) * C::ROWB,
-                          uint32_t(n) * C::ROWB, bar, policy);
+            mbar_arrive_expect_tx(bar, uint32_t(KVH * n) * C::ROWB);
+#pragma unroll
+            for (int kv = 0; kv < KVH; ++kv)
+                bulk_copy_g2s(slot + kv * C::HEAD_BYTES,
+                              rows + ((int64_t(b) * heads + g + kv) * p.cap + t.row()) * C::ROWB,
+                              uint32_t(n) * C::ROWB, bar, policy);
         }
     } else {
         const int64_t n_req = p.pos[b];
         const int64_t Lk = n_req > 0 ? n_req + p.sink_len : 0;
         const bool split = p.W > 0 && Lk > int64_t(p.S) + p.W;  // sinks, then the last W keys
-        const int64_t row = t.row() + lane;
+        const int i = lane % C::TR, kv = lane / C::TR;
+        const int64_t row = t.row() + i;
         const int64_t key = split && row >= p.S ? Lk - p.W + (row - p.S) : row;
-        const bool active = lane < n;
+        const bool active = i < n;
         int64_t blk = 0;
         if (active) {
             if (key < p.sink_len) {
@@ -189,36 +216,40 @@ __device__ __forceinline__ void load_tile(const DecodeParams& p, const Walk& t, 
             }
         }
         const int64_t in = key & (p.bs - 1);
-        const bool first = active && (lane == 0 || in == 0 || (split && row == p.S));
+        const bool first = active && (i == 0 || in == 0 || (split && row == p.S));
         const uint32_t firsts = __ballot_sync(kFull, first);
-        if (lane == 0) mbar_arrive_expect_tx(bar, uint32_t(n) * C::ROWB);
+        if (lane == 0) mbar_arrive_expect_tx(bar, uint32_t(KVH * n) * C::ROWB);
         __syncwarp();
         if (first) {
-            const uint32_t later = lane == 31 ? 0u : firsts >> (lane + 1);
-            const int len = later != 0 ? __ffs(int(later)) : n - lane;
-            bulk_copy_g2s(slot + lane * C::ROWB, rows + ((blk * p.Hkv + g) * p.bs + in) * C::ROWB,
-                          uint32_t(len) * C::ROWB, bar, policy);
+            // rows up to the next run of this kv head, or to the tile's end
+            const uint32_t later = (lane == 31 ? 0u : firsts >> (lane + 1)) & ((1u << (C::TR - 1 - i)) - 1u);
+            const int len = later != 0 ? __ffs(int(later)) : n - i;
+            bulk_copy_g2s(slot + kv * C::HEAD_BYTES + i * C::ROWB,
+                          rows + ((blk * heads + g + kv) * p.bs + in) * C::ROWB, uint32_t(len) * C::ROWB, bar,
+                          policy);
         }
     }
 }
 
-// The online softmax state of one warp over a unit, for the lane's heads 2t, 2t + 1.
+// The online softmax state of one warp over a unit, for the lane's columns 2t, 2t + 1.
 template <int NG> struct State4 {
     float o[NG][2][4];    // group, dim pair i of the lane's 4 dims (4 g + 2 i + {0, 1}): (dim, head) products
     float2 om[NG];        // sum of weight * m
     float2 l;             // sum of weights (this lane's rows)
     float2 ref;           // reference score of each head (the same in all lanes of a t)
+    float2 limit;         // raw score that outgrows it
     int vexp;             // exponent of the V scale in the reference (the same in all lanes)
 };
 
-template <typename T, int D, int NREP, bool PAGED>
-__global__ void __launch_bounds__(Cfg4<D, NREP>::THREADS, 1) decode4_split_kernel(DecodeParams p) {
-    using C = Cfg4<D, NREP>;
-    constexpr int NG = C::NG, NWARPS = C::NWARPS, SLOTS = C::SLOTS;
+template <typename T, int D, int NREP, int KVH, bool PAGED>
+__global__ void __launch_bounds__(Cfg4<D, NREP, KVH>::THREADS, 1) decode4_split_kernel(DecodeParams p) {
+    using C = Cfg4<D, NREP, KVH>;
+    constexpr int NG = C::NG, NWARPS = C::NWARPS, SLOTS = C::SLOTS, TR = C::TR, HEADS = C::HEADS;
     constexpr bool F32 = std::is_same<T, float>::value;
-    constexpr int NQ = F32 ? 2 : 1;  // fp16 parts of q and of P'
+    static_assert(!F32 || KVH == 1, "fp32 calls: registers for one kv head's q");
+    constexpr int NQ = F32 ? 2 : 1;          // fp16 parts of q and of P'
+    constexpr int NM = KVH == 1 ? 2 : 1;     // 16-row matrix tiles of scores
     extern __shared__ __align__(128) uint8_t smem[];
-    uint8_t* zero_row = smem + C::OFF_ZERO;
     float* merge = reinterpret_cast<float*>(smem + C::OFF_MERGE);
     int64_t* pre = reinterpret_cast<int64_t*>(smem + C::OFF_PRE);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -230,7 +261,6 @@ __global__ void __launch_bounds__(Cfg4<D, NREP>::THREADS, 1) decode4_split_kerne
         for (int s = 0; s < SLOTS; ++s) mbar_init(&bars[s], 1);
         fence_barrier_init();
     }
-    for (int i = threadIdx.x; i < C::ROWB / 4; i += C::THREADS) reinterpret_cast<uint32_t*>(zero_row)[i] = 0;
     pdl_wait();  // the append before this kernel has written the state, q and the new rows
     if (warp == 0) unit_prefix(p, pre, lane);
     __syncthreads();
@@ -244,36 +274,49 @@ __global__ void __launch_bounds__(Cfg4<D, NREP>::THREADS, 1) decode4_split_kerne
     const uint64_t policy = l2_policy_evict_first();
     bool timed_out = false, bad = false;
 
-    TileWalk<NWARPS> ld, w;
+    TileWalk<NWARPS, TR> ld, w;
     w.begin(pre, p.B, p.Hkv, lo, hi, cap, warp);
     ld = w;
     bool more = ld.settle(warp);
     int slot = 0;
     uint32_t phase = 0;
     for (int s = 0; s < SLOTS && more; ++s) {
-        load_tile<C, PAGED>(p, ld, ring + s * C::SLOT_BYTES, &bars[s], policy, lane, &bad);
+        load_tile<C, KVH, PAGED>(p, ld, ring + s * C::SLOT_BYTES, &bars[s], policy, lane, &bad);
         ld.k += NWARPS;
         more = ld.settle(warp);
     }
 
     const uint32_t half_sel = (g8 & 1) ? 0x7632u : 0x5410u;  // which 4 codes of a word of 8 are this lane's
+    const int my_kv = KVH == 1 ? 0 : t4 >> 1;                // kv head of the lane's columns
+    // this lane's places in a slot: K words of row kappa(g8), parameters of that row (of the
+    // columns' kv head), V words of rows kappa(2 t4) and kappa(2 t4 + 1)
+    const int k_at = kappa(g8) * C::ROWB + kv4_word_offset(D, t4, 0);
+    const int par_at = kappa(g8) * C::ROWB + my_kv * C::HEAD_BYTES + kv4_param_offset(D, 0);
+    const int v_at0 = kappa(2 * t4) * C::ROWB + kv4_half_bytes(D) + kv4_word_offset(D, g8 >> 1, 0);
+    const int v_at1 = kappa(2 * t4 + 1) * C::ROWB + kv4_half_bytes(D) + kv4_word_offset(D, g8 >> 1, 0);
+    // the N side column g8 belongs to kv head g8 / 4 (KVH = 2): a product with one kv head's
+    // codes takes zeros in the other's columns (P' is multiplied by 1 or 0)
+    const __half2 keep[2] = {__float2half2_rn(KVH == 1 || g8 < 4 ? 1.0f : 0.0f),
+                             __float2half2_rn(g8 < 4 ? 0.0f : 1.0f)};
     do {
         const int b = w.w.b, g = w.w.g;
         const int64_t unit = int64_t(b) * p.Hkv + g;
-        // ---- q as the N-side operand: head g8, dims 32 grp + 8 t4 .. + 7 ----
-        uint32_t qb[NQ][NG][4];
-        float fac;  // score units (log2) per accumulator unit, of head g8
+        // ---- q as the N-side operand: column g8, dims 32 grp + 8 t4 .. + 7 ----
+        uint32_t qb[KVH][NQ][NG][4];
+        float fac;  // score units (log2) per accumulator unit, of column g8
         {
+            const int qh = KVH == 1 ? g8 : (g8 >> 2) * NREP + (g8 & 3);
+            const bool real = KVH == 1 ? g8 < NREP : (g8 & 3) < NREP;
             float qf[NG][8];
             float amax = 0.0f;
-            const T* qrow = static_cast<const T*>(p.q) + (unit * NREP + g8) * D;
+            const T* qrow = static_cast<const T*>(p.q) + (unit * HEADS + qh) * D;
 #pragma unroll
             for (int r = 0; r < NG; ++r) {
                 constexpr int V = ElemIO<T>::kPerVec;
 #pragma unroll
                 for (int i = 0; i < 8 / V; ++i) {
-                    const uint4 raw = g8 < NREP ? reinterpret_cast<const uint4*>(qrow + 32 * r + 8 * t4)[i]
-                                                : make_uint4(0, 0, 0, 0);
+                    const uint4 raw = real ? reinterpret_cast<const uint4*>(qrow + 32 * r + 8 * t4)[i]
+                                           : make_uint4(0, 0, 0, 0);
                     ElemIO<T>::unpack(raw, qf[r] + V * i);
                 }
 #pragma unroll
@@ -292,10 +335,12 @@ __global__ void __launch_bounds__(Cfg4<D, NREP>::THREADS, 1) decode4_split_kerne
                     float x = qf[r][i] * ((i & 1) ? f1 : f0), y = qf[r][i + 4] * ((i & 1) ? f1 : f0);
 #pragma unroll
                     for (int h = 0; h < NQ; ++h) {
-                        qb[h][r][i] = half2_bits(x, y);
-                        const float2 part = half2_floats(qb[h][r][i]);
+                        const uint32_t bits = half2_bits(x, y);
+                        const float2 part = half2_floats(bits);
                         x -= part.x;
                         y -= part.y;
+#pragma unroll
+                        for (int kv = 0; kv < KVH; ++kv) qb[kv][h][r][i] = KVH == 1 || (g8 >> 2) == kv ? bits : 0u;
                     }
                 }
         }
@@ -306,10 +351,13 @@ __global__ void __launch_bounds__(Cfg4<D, NREP>::THREADS, 1) decode4_split_kerne
         for (int r = 0; r < NG; ++r) {
             float a[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int h = 0; h < NQ; ++h)
+            for (int kv = 0; kv < KVH; ++kv)
 #pragma unroll
-                for (int i = 0; i < 4; i += 2)
-                    mma16816(a, 0x00010001u, 0x00010001u, 0x00100010u, 0x00100010u, qb[h][r][i], qb[h][r][i + 1]);
+                for (int h = 0; h < NQ; ++h)
+#pragma unroll
+                    for (int i = 0; i < 4; i += 2)
+                        mma16816(a, 0x00010001u, 0x00010001u, 0x00100010u, 0x00100010u, qb[kv][h][r][i],
+                                 qb[kv][h][r][i + 1]);
             qsum[r] = make_float2(a[0], a[1]);
         }
 
@@ -324,69 +372,87 @@ __global__ void __launch_bounds__(Cfg4<D, NREP>::THREADS, 1) decode4_split_kerne
         }
         st.l = make_float2(0.f, 0.f);
         st.ref = make_float2(kRefNone, kRefNone);
+        st.limit = make_float2(-INFINITY, -INFINITY);
         st.vexp = kExpFloor;
 
         for (; w.k < w.nt; w.k += NWARPS) {
             const int n = w.rows();
-            const uint8_t* tile = ring + slot * C::SLOT_BYTES;
+            uint8_t* tile = ring + slot * C::SLOT_BYTES;
             if (!mbar_wait_bounded(&bars[slot], phase)) timed_out = true;
-
-            // ---- scores: row m of matrix tile mt is tile row 16 mt + 8 (m / 8) + kappa(m % 8) ----
-            const int kr = kappa(g8);
-            float2 sc[4];         // [2 mt + row half]: the lane's two heads
-            uint32_t vpar[4][NG]; // V (m, s) of the same rows
+            if (n < TR) {  // rows past the tile's last one: zeros (whatever the slot held)
 #pragma unroll
-            for (int mt = 0; mt < 2; ++mt) {
-                uint32_t kw[2][NG], kp[2][NG];
+                for (int kv = 0; kv < KVH; ++kv)
+                    for (int i = n * C::ROWB + lane * 16; i < C::HEAD_BYTES; i += 512)
+                        *reinterpret_cast<uint4*>(tile + kv * C::HEAD_BYTES + i) = make_uint4(0, 0, 0, 0);
+                __syncwarp();
+            }
+
+            // ---- scores: row m of matrix tile j is tile row 16 j + 8 (m / 8) + kappa(m % 8) ----
+            float2 sc[2 * NM];         // [2 j + row half]: the lane's two columns, accumulator units
+            uint32_t vpar[2 * NM][NG]; // V (m, s) of the same rows
+#pragma unroll
+            for (int j = 0; j < NM; ++j) {
+                const uint8_t* base = tile + 16 * j * C::ROWB;
+                float a[NG][4];
+#pragma unroll
+                for (int kv = 0; kv < KVH; ++kv) {
+                    uint32_t kw[2][NG];
+                    load_words<NG>(base + kv * C::HEAD_BYTES + k_at, kw[0]);
+                    load_words<NG>(base + kv * C::HEAD_BYTES + k_at + 8 * C::ROWB, kw[1]);
+#pragma unroll
+                    for (int r = 0; r < NG; ++r) {
+                        const uint32_t x = kw[0][r] >> 8, y = kw[1][r] >> 8;
+#pragma unroll
+                        for (int h = NQ - 1; h >= 0; --h) {  // the small part first
+                            if (kv == 0 && h == NQ - 1)
+                                mma16816_first(a[r], kw[0][r] & kLowNibbles, kw[1][r] & kLowNibbles,
+                                               kw[0][r] & kHighNibbles, kw[1][r] & kHighNibbles, qb[kv][h][r][0],
+                                               qb[kv][h][r][1]);
+                            else
+                                mma16816(a[r], kw[0][r] & kLowNibbles, kw[1][r] & kLowNibbles,
+                                         kw[0][r] & kHighNibbles, kw[1][r] & kHighNibbles, qb[kv][h][r][0],
+                                         qb[kv][h][r][1]);
+                            mma16816(a[r], x & kLowNibbles, y & kLowNibbles, x & kHighNibbles, y & kHighNibbles,
+                                     qb[kv][h][r][2], qb[kv][h][r][3]);
+                        }
+                    }
+                }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const int r = 16 * mt + 8 * h + kr;
-                    const uint8_t* row = r < n ? tile + r * C::ROWB : zero_row;
-                    load_words<NG>(row + kv4_word_offset(D, t4, 0), kw[h]);
-                    load_words<NG>(row + kv4_param_offset(D, 0), kp[h]);
-                    load_words<NG>(row + kv4_half_bytes(D) + kv4_param_offset(D, 0), vpar[2 * mt + h]);
-                }
-                float2 s0 = make_float2(0.f, 0.f), s1 = s0;
+                    const uint8_t* row = base + par_at + 8 * h * C::ROWB;
+                    uint32_t kp[NG];
+                    load_words<NG>(row, kp);
+                    load_words<NG>(row + kv4_half_bytes(D), vpar[2 * j + h]);
+                    float2 s0 = make_float2(0.f, 0.f);
 #pragma unroll
-                for (int r = 0; r < NG; ++r) {
-                    float a[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int h = 0; h < NQ; ++h) {
-                        mma16816(a, kw[0][r] & kLowNibbles, kw[1][r] & kLowNibbles, kw[0][r] & kHighNibbles,
-                                 kw[1][r] & kHighNibbles, qb[h][r][0], qb[h][r][1]);
-                        const uint32_t x = kw[0][r] >> 8, y = kw[1][r] >> 8;
-                        mma16816(a, x & kLowNibbles, y & kLowNibbles, x & kHighNibbles, y & kHighNibbles,
-                                 qb[h][r][2], qb[h][r][3]);
+                    for (int r = 0; r < NG; ++r) {
+                        const float s = __uint_as_float(kp[r] & 0xFFFF0000u), m = __uint_as_float(kp[r] << 16);
+                        s0 = __ffma2_rn(make_float2(s, s), make_float2(a[r][2 * h], a[r][2 * h + 1]), s0);
+                        s0 = __ffma2_rn(make_float2(m, m), qsum[r], s0);
                     }
-                    const float ka = __uint_as_float(kp[0][r] & 0xFFFF0000u), ma = __uint_as_float(kp[0][r] << 16);
-                    const float kb = __uint_as_float(kp[1][r] & 0xFFFF0000u), mb = __uint_as_float(kp[1][r] << 16);
-                    s0 = __ffma2_rn(make_float2(ka, ka), make_float2(a[0], a[1]), s0);
-                    s1 = __ffma2_rn(make_float2(kb, kb), make_float2(a[2], a[3]), s1);
-                    s0 = __ffma2_rn(make_float2(ma, ma), qsum[r], s0);
-                    s1 = __ffma2_rn(make_float2(mb, mb), qsum[r], s1);
+                    sc[2 * j + h] = s0;
                 }
-                sc[2 * mt] = __fmul2_rn(s0, fac2);
-                sc[2 * mt + 1] = __fmul2_rn(s1, fac2);
             }
-            if (n < kTileRows) {
+            if (n < TR) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (16 * (i >> 1) + 8 * (i & 1) + kr >= n) sc[i] = make_float2(-INFINITY, -INFINITY);
+                for (int i = 0; i < 2 * NM; ++i)
+                    if (8 * i + kappa(g8) >= n) sc[i] = make_float2(-INFINITY, -INFINITY);
             }
 
             // ---- reference: moved when a score or a V scale outgrows it ----
-            float2 top = make_float2(fmaxf(fmaxf(sc[0].x, sc[1].x), fmaxf(sc[2].x, sc[3].x)),
-                                     fmaxf(fmaxf(sc[0].y, sc[1].y), fmaxf(sc[2].y, sc[3].y)));
+            float2 top = sc[0];
             uint32_t vtop = 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 2 * NM; ++i) {
+                top = make_float2(fmaxf(top.x, sc[i].x), fmaxf(top.y, sc[i].y));
 #pragma unroll
                 for (int r = 0; r < NG; ++r) vtop = max(vtop, vpar[i][r]);
-            const bool outgrown = top.x > st.ref.x + kSlack || top.y > st.ref.y + kSlack ||
-                                  int(vtop >> 23) - 127 > st.vexp;
+            }
+            const bool outgrown = top.x > st.limit.x || top.y > st.limit.y || int(vtop >> 23) - 127 > st.vexp;
             if (__any_sync(kFull, outgrown)) {
                 const float2 old = st.ref;
                 const int old_exp = st.vexp;
+                top = __fmul2_rn(top, fac2);
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) {
                     top.x = fmaxf(top.x, __shfl_xor_sync(kFull, top.x, o));
@@ -395,12 +461,13 @@ __global__ void __launch_bounds__(Cfg4<D, NREP>::THREADS, 1) decode4_split_kerne
                 // a non-finite scale spoils its own group and is kept out of the reference
                 vtop = 0;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < 2 * NM; ++i)
 #pragma unroll
                     for (int r = 0; r < NG; ++r) vtop = max(vtop, vpar[i][r] < 0x7F800000u ? vpar[i][r] : 0u);
                 vtop = __reduce_max_sync(kFull, vtop);
                 st.ref.x = fmaxf(st.ref.x, top.x);
                 st.ref.y = fmaxf(st.ref.y, top.y);
+                st.limit = make_float2((st.ref.x + kSlack) / fac2.x, (st.ref.y + kSlack) / fac2.y);
                 st.vexp = max(st.vexp, int(vtop >> 23) - 127);
                 const float de = float(old_exp - st.vexp);
                 const float2 al = make_float2(fast_exp2_approx(old.x - st.ref.x + de),
@@ -420,32 +487,38 @@ __global__ void __launch_bounds__(Cfg4<D, NREP>::THREADS, 1) decode4_split_kerne
             }
 
             // ---- weights, and their products with V ----
-            const float shift = float(kHead - st.vexp);
+            // fp32 calls take the power of two after the exponential: the argument is then near
+            // 0 for the largest weights, and its rounding with it
+            const float shift = F32 ? 0.0f : float(kHead - st.vexp);
             const float2 off = make_float2(shift - st.ref.x, shift - st.ref.y);
+            const float after = pow2f(min(kHead - st.vexp, 127));
 #pragma unroll
-            for (int mt = 0; mt < 2; ++mt) {
+            for (int j = 0; j < NM; ++j) {
                 float2 pr[2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const float2 x = __fadd2_rn(sc[2 * mt + h], off);
+                    const float2 x = __ffma2_rn(sc[2 * j + h], fac2, off);
                     pr[h] = make_float2(fast_exp2_approx(x.x), fast_exp2_approx(x.y));
+                    if constexpr (F32) pr[h] = __fmul2_rn(pr[h], make_float2(after, after));
                     st.l = __fadd2_rn(st.l, pr[h]);
                 }
                 // this lane's keys as the K side of the second product: 2t, 2t + 1 and + 8
-                uint32_t vw[4][NG];
+                uint32_t vw[KVH][4][NG];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = 16 * mt + 8 * (i >> 1) + kappa(2 * t4 + (i & 1));
-                    const uint8_t* row = r < n ? tile + r * C::ROWB : zero_row;
-                    load_words<NG>(row + kv4_half_bytes(D) + kv4_word_offset(D, g8 >> 1, 0), vw[i]);
+                for (int kv = 0; kv < KVH; ++kv) {
+                    const uint8_t* base = tile + kv * C::HEAD_BYTES + 16 * j * C::ROWB;
+                    load_words<NG>(base + v_at0, vw[kv][0]);
+                    load_words<NG>(base + v_at1, vw[kv][1]);
+                    load_words<NG>(base + v_at0 + 8 * C::ROWB, vw[kv][2]);
+                    load_words<NG>(base + v_at1 + 8 * C::ROWB, vw[kv][3]);
                 }
 #pragma unroll
                 for (int r = 0; r < NG; ++r) {
                     uint32_t pb[NQ][2];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const float s = __uint_as_float(vpar[2 * mt + h][r] & 0xFFFF0000u);
-                        const float m = __uint_as_float(vpar[2 * mt + h][r] << 16);
+                        const float s = __uint_as_float(vpar[2 * j + h][r] & 0xFFFF0000u);
+                        const float m = __uint_as_float(vpar[2 * j + h][r] << 16);
                         float2 ps = __fmul2_rn(pr[h], make_float2(s, s));
                         st.om[r] = __ffma2_rn(pr[h], make_float2(m, m), st.om[r]);
 #pragma unroll
@@ -456,20 +529,28 @@ __global__ void __launch_bounds__(Cfg4<D, NREP>::THREADS, 1) decode4_split_kerne
                             ps = make_float2(ps.x - part.x, ps.y - part.y);
                         }
                     }
-                    const uint32_t x = __byte_perm(vw[0][r], vw[1][r], half_sel);
-                    const uint32_t y = __byte_perm(vw[2][r], vw[3][r], half_sel);
 #pragma unroll
-                    for (int q = 0; q < NQ; ++q) {
-                        mma16816(st.o[r][0], x & kLowNibbles, x & kHighNibbles, y & kLowNibbles, y & kHighNibbles,
-                                 pb[q][0], pb[q][1]);
-                        mma16816(st.o[r][1], (x >> 8) & kLowNibbles, (x >> 8) & kHighNibbles, (y >> 8) & kLowNibbles,
-                                 (y >> 8) & kHighNibbles, pb[q][0], pb[q][1]);
+                    for (int kv = 0; kv < KVH; ++kv) {
+                        const uint32_t x = __byte_perm(vw[kv][0][r], vw[kv][1][r], half_sel);
+                        const uint32_t y = __byte_perm(vw[kv][2][r], vw[kv][3][r], half_sel);
+                        const uint32_t xs = x >> 8, ys = y >> 8;
+#pragma unroll
+                        for (int q = 0; q < NQ; ++q) {
+                            const uint32_t b0 = KVH == 1 ? pb[q][0] : half2_times(pb[q][0], keep[kv]);
+                            const uint32_t b1 = KVH == 1 ? pb[q][1] : half2_times(pb[q][1], keep[kv]);
+                            mma16816(st.o[r][0], x & kLowNibbles, x & kHighNibbles, y & kLowNibbles,
+                                     y & kHighNibbles, b0, b1);
+                            mma16816(st.o[r][1], xs & kLowNibbles, xs & kHighNibbles, ys & kLowNibbles,
+                                     ys & kHighNibbles, b0, b1);
+                        }
                     }
                 }
             }
-            __syncwarp();  // the slot has been read
+            // the slot has been read; zeros written to it come before the next copy
+            if (n < TR) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
             if (more) {
-                load_tile<C, PAGED>(p, ld, ring + slot * C::SLOT_BYTES, &bars[slot], policy, lane, &bad);
+                load_tile<C, KVH, PAGED>(p, ld, tile, &bars[slot], policy, lane, &bad);
                 ld.k += NWARPS;
                 more = ld.settle(warp);
             }
@@ -487,87 +568,121 @@ __global__ void __launch_bounds__(Cfg4<D, NREP>::THREADS, 1) decode4_split_kerne
                 st.om[r].y += __shfl_xor_sync(kFull, st.om[r].y, o);
             }
         }
-        float* mw = merge + warp * C::MERGE_FLOATS;
-        const float mshift = float(st.vexp - kHead);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int h = 2 * t4 + e;
-            if (h < NREP) {
-                if (g8 == 0) {
-                    const float ref = e ? st.ref.y : st.ref.x;
-                    mw[h] = ref == kRefNone ? -INFINITY : ref + mshift;
-                    mw[NREP + h] = e ? st.l.y : st.l.x;
-                }
-#pragma unroll
-                for (int r = 0; r < NG; ++r) {
-                    const float m = e ? st.om[r].y : st.om[r].x;
-                    float4 v;
-                    v.x = fmaf(st.o[r][0][e], 16777216.0f, m);        // 2^24: even nibbles
-                    v.y = fmaf(st.o[r][0][2 + e], 1048576.0f, m);     // 2^20: odd nibbles
-                    v.z = fmaf(st.o[r][1][e], 16777216.0f, m);
-                    v.w = fmaf(st.o[r][1][2 + e], 1048576.0f, m);
-                    float* d = mw + 2 * NREP + h * D + 32 * r + 4 * g8;
-                    reinterpret_cast<float2*>(d)[0] = make_float2(v.x, v.y);
-                    reinterpret_cast<float2*>(d)[1] = make_float2(v.z, v.w);
-                }
-            }
-        }
-        __syncthreads();
         float* outp = p.ws + (unit + c) * C::PARTIAL_FLOATS;
-        for (int idx = threadIdx.x; idx < NREP * D; idx += C::THREADS) {
-            const int h = idx / D;
-            float M = -INFINITY;
+        const float mshift = float(st.vexp - kHead);
+        constexpr int PER = (HEADS * D + C::THREADS - 1) / C::THREADS;  // values of the partial per thread
+        float acc[PER], accM[PER], accL[PER];
 #pragma unroll
-            for (int ww = 0; ww < NWARPS; ++ww) M = fmaxf(M, merge[ww * C::MERGE_FLOATS + h]);
-            const float Mu = M == -INFINITY ? 0.0f : M;
-            float a = 0.0f, lsum = 0.0f;
+        for (int i = 0; i < PER; ++i) {
+            acc[i] = accL[i] = 0.0f;
+            accM[i] = -INFINITY;
+        }
+        for (int round = 0; round < C::MERGE_ROUNDS; ++round) {
+            if (warp / C::MERGE_WARPS == round) {
+                float* mw = merge + (warp % C::MERGE_WARPS) * C::MERGE_FLOATS;
 #pragma unroll
-            for (int ww = 0; ww < NWARPS; ++ww) {
-                const float* mm = merge + ww * C::MERGE_FLOATS;
-                const float f = fast_exp2_approx(mm[h] - Mu);
-                a = fmaf(f, mm[2 * NREP + idx], a);
-                lsum = fmaf(f, mm[NREP + h], lsum);
+                for (int e = 0; e < 2; ++e) {
+                    const int col = 2 * t4 + e;
+                    const int h = KVH == 1 ? col : (col >> 2) * NREP + (col & 3);
+                    if (KVH == 1 ? col < NREP : (col & 3) < NREP) {
+                        if (g8 == 0) {
+                            const float ref = e ? st.ref.y : st.ref.x;
+                            mw[h] = ref == kRefNone ? -INFINITY : ref + mshift;
+                            mw[HEADS + h] = e ? st.l.y : st.l.x;
+                        }
+#pragma unroll
+                        for (int r = 0; r < NG; ++r) {
+                            const float m = e ? st.om[r].y : st.om[r].x;
+                            float4 v;
+                            v.x = fmaf(st.o[r][0][e], 16777216.0f, m);        // 2^24: even nibbles
+                            v.y = fmaf(st.o[r][0][2 + e], 1048576.0f, m);     // 2^20: odd nibbles
+                            v.z = fmaf(st.o[r][1][e], 16777216.0f, m);
+                            v.w = fmaf(st.o[r][1][2 + e], 1048576.0f, m);
+                            float* d = mw + 2 * HEADS + h * D + 32 * r + 4 * g8;
+                            reinterpret_cast<float2*>(d)[0] = make_float2(v.x, v.y);
+                            reinterpret_cast<float2*>(d)[1] = make_float2(v.z, v.w);
+                        }
+                    }
+                }
             }
-            outp[2 * NREP + idx] = a;
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const int idx = threadIdx.x + i * C::THREADS;
+                if (idx >= HEADS * D) break;
+                const int h = idx / D;
+                float M = accM[i];
+#pragma unroll
+                for (int ww = 0; ww < C::MERGE_WARPS; ++ww) M = fmaxf(M, merge[ww * C::MERGE_FLOATS + h]);
+                const float Mu = M == -INFINITY ? 0.0f : M;
+                const float f0 = fast_exp2_approx(accM[i] - Mu);
+                float a = acc[i] * f0, lsum = accL[i] * f0;
+#pragma unroll
+                for (int ww = 0; ww < C::MERGE_WARPS; ++ww) {
+                    const float* mm = merge + ww * C::MERGE_FLOATS;
+                    const float f = fast_exp2_approx(mm[h] - Mu);
+                    a = fmaf(f, mm[2 * HEADS + idx], a);
+                    lsum = fmaf(f, mm[HEADS + h], lsum);
+                }
+                acc[i] = a;
+                accL[i] = lsum;
+                accM[i] = M;
+            }
+            __syncthreads();
+        }
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int idx = threadIdx.x + i * C::THREADS;
+            if (idx >= HEADS * D) break;
+            outp[2 * HEADS + idx] = acc[i];
             if (idx % D == 0) {
-                outp[h] = M;
-                outp[NREP + h] = lsum;
+                outp[idx / D] = accM[i];
+                outp[HEADS + idx / D] = accL[i];
             }
         }
-        __syncthreads();
     } while (w.next_unit(warp));
     if (timed_out) set_error(p.err, SK_DEVERR_TIMEOUT);
     if (bad) set_error(p.err, SK_DEVERR_BLOCK_TABLE);
 }
 
-template <typename T, int D, int NREP, bool PAGED>
+template <typename T, int D, int NREP, int KVH, bool PAGED>
 cudaError_t run4(DecodeParams p, int64_t rows_most, cudaStream_t st) {
-    using C = Cfg4<D, NREP>;
+    using C = Cfg4<D, NREP, KVH>;
+    constexpr int HEADS = C::HEADS;
     static PerDevice<cudaError_t> attr;
-    const cudaError_t a = set_smem_limit_once(attr, decode4_split_kernel<T, D, NREP, PAGED>, int(C::SMEM));
+    const cudaError_t a = set_smem_limit_once(attr, decode4_split_kernel<T, D, NREP, KVH, PAGED>, int(C::SMEM));
     if (a != cudaSuccess) return a;
+    p.Hkv /= KVH;  // units of KVH kv heads, HEADS q heads each, for both kernels
     const int64_t units = int64_t(p.B) * p.Hkv;
     // no more blocks than rows the cache can hold: they would only add partials to skip
-    p.n_blocks = int(std::max<int64_t>(1, std::min<int64_t>(device_sm_count(), rows_most)));
-    cudaError_t e = launch_pdl(decode4_split_kernel<T, D, NREP, PAGED>, dim3(p.n_blocks), dim3(C::THREADS), C::SMEM,
-                               st, p);
+    p.n_blocks = int(std::max<int64_t>(1, std::min<int64_t>(device_sm_count(), rows_most / KVH)));
+    cudaError_t e = launch_pdl(decode4_split_kernel<T, D, NREP, KVH, PAGED>, dim3(p.n_blocks), dim3(C::THREADS),
+                               C::SMEM, st, p);
     if (e != cudaSuccess) return e;
     p.combine_wpu = combine_wpu(p.n_blocks, units);
-    const int64_t warps = units * NREP * p.combine_wpu;
+    const int64_t warps = units * HEADS * p.combine_wpu;
     return p.combine_wpu == 1
-               ? launch_pdl(decode_combine_kernel<T, D, NREP>, dim3(unsigned((warps + 7) / 8)), dim3(256), 0, st, p)
-               : launch_pdl(decode_combine_group_kernel<T, D, NREP>, dim3(unsigned((warps + 7) / 8)), dim3(256), 0,
+               ? launch_pdl(decode_combine_kernel<T, D, HEADS>, dim3(unsigned((warps + 7) / 8)), dim3(256), 0, st, p)
+               : launch_pdl(decode_combine_group_kernel<T, D, HEADS>, dim3(unsigned((warps + 7) / 8)), dim3(256), 0,
                             st, p);
 }
 
 template <typename T, int D>
 bool dispatch4(int nrep, const DecodeParams& p, int64_t rows_most, cudaStream_t st, cudaError_t* e) {
     const bool paged = p.kind == kKindPaged;
+    constexpr bool f32 = std::is_same<T, float>::value;
+    // Two kv heads to a unit where they fill the 8 columns better: the work per score and per
+    // weight (scales, exponentials, rounding, transposing) is then done once for both.
+    const bool pair = !f32 && p.Hkv % 2 == 0;
     switch (nrep) {
-#define SK_CASE(N)                                                        \
-    case N:                                                               \
-        *e = paged ? run4<T, D, N, true>(p, rows_most, st)                \
-                   : run4<T, D, N, false>(p, rows_most, st);              \
+#define SK_CASE(N)                                                                              \
+    case N:                                                                                     \
+        if (pair && N <= 4)                                                                     \
+            *e = paged ? run4<T, D, N, (N <= 4 && !f32) ? 2 : 1, true>(p, rows_most, st)        \
+                       : run4<T, D, N, (N <= 4 && !f32) ? 2 : 1, false>(p, rows_most, st);      \
+        else                                                                                    \
+            *e = paged ? run4<T, D, N, 1, true>(p, rows_most, st)                               \
+                       : run4<T, D, N, 1, false>(p, rows_most, st);                             \
         return true;
         SK_CASE(1)
         SK_CASE(2)
@@ -583,7 +698,10 @@ bool dispatch4(int nrep, const DecodeParams& p, int64_t rows_most, cudaStream_t 
 
 size_t kv4_decode_workspace(int batch, int n_kv_heads, int head_dim, int nrep) {
     if ((head_dim != 64 && head_dim != 128) || (nrep != 1 && nrep != 2 && nrep != 4 && nrep != 8)) return 0;
-    return size_t(device_sm_count() + int64_t(batch) * n_kv_heads) * nrep * (head_dim + 2) * sizeof(float);
+    // a slot per block and unit; a unit has the q heads of up to two kv heads
+    const int pair = nrep <= 4 && n_kv_heads % 2 == 0 ? 2 : 1;
+    return size_t(int64_t(device_sm_count()) * pair + int64_t(batch) * n_kv_heads) * nrep * (head_dim + 2) *
+           sizeof(float);
 }
 
 bool kv4_decode_run(const Kv4DecodeArgs& a, cudaStream_t st, cudaError_t* e) {

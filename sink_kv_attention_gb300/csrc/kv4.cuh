@@ -50,10 +50,18 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return y;
 }
 
+// x / d for a divisor whose reciprocal is held in two parts, inv + lo = 1/d to 2^-47: one
+// rounding of a product that is off by 2^-47, so the quotient is the correctly rounded one
+// unless x / d is that close to the middle of two floats, and exact where x / d is a float
+// (the ties of rint, and quotients that are bf16 values, among them).
+__device__ __forceinline__ float div_by(float x, float inv, float lo) { return fmaf(x, inv, x * lo); }
+
 // (m, s) of a group with extremes lo and hi.
 __device__ __forceinline__ void kv4_group_params(float lo, float hi, float* m, float* s) {
+    constexpr float inv15 = 1.0f / 15.0f;                        // nearest float
+    constexpr float lo15 = float(1.0 / 15.0 - double(inv15));
     *m = bf16_floor(lo);
-    *s = bf16_ceil_nonneg(__fdiv_rn(hi - *m, 15.0f));
+    *s = bf16_ceil_nonneg(div_by(hi - *m, inv15, lo15));
 }
 
 // The pair as stored: m in the low half of the word, s in the high half.
@@ -66,10 +74,27 @@ __device__ __forceinline__ uint32_t kv4_code(float x, float m, float s) {
     return uint32_t(fminf(fmaxf(r, 0.0f), 15.0f));    // NaN -> 0
 }
 
-// Codes of n <= 8 values as nibbles 0 .. n - 1.
+// Codes of N (4 or 8) values of a group as nibbles 0 .. N - 1.  Where s is neither tiny nor
+// huge the quotients are products with 1/s (div_by), in [0, 15] because s was rounded up.
+// Adding 1.5 * 2^23 rounds them (half to even) and leaves the code in the low bits under a
+// constant, and the constants of all nibbles are taken off the sum at once.
 template <int N>
 __device__ __forceinline__ uint32_t kv4_codes(const float* x, float m, float s) {
     uint32_t w = 0;
+    if (s >= 7.9e-31f && s <= 1.2e27f) {  // 2^-100, 2^90: no part of 1/s underflows
+        const float inv = __frcp_rn(s);
+        const float lo = fmaf(-s, inv, 1.0f) * inv;
+        const float2 m2 = make_float2(-m, -m), inv2 = make_float2(inv, inv), lo2 = make_float2(lo, lo);
+        const float2 magic = make_float2(12582912.0f, 12582912.0f);
+        constexpr uint32_t kMagicSum = 0x4B400000u * (N == 8 ? 0x11111111u : 0x1111u);
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+            const float2 t = __fadd2_rn(make_float2(x[i], x[i + 1]), m2);
+            const float2 y = __fadd2_rn(__ffma2_rn(t, inv2, __fmul2_rn(t, lo2)), magic);
+            w += (__float_as_uint(y.x) << (4 * i)) + (__float_as_uint(y.y) << (4 * i + 4));
+        }
+        return w - kMagicSum;
+    }
 #pragma unroll
     for (int i = 0; i < N; ++i) w |= kv4_code(x[i], m, s) << (4 * i);
     return w;

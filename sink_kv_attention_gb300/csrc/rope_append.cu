@@ -382,10 +382,12 @@ __global__ void __launch_bounds__(kThreads + 32) kv_append_kernel(AppendParams p
                 const bool store_kv = live && which != 0 && crw.ok;
                 if constexpr (std::is_same<KC, Kv4>::value) {
                     // 4-bit rows: the key as it was left in k, the value as given
-                    ElemIO<IO>::unpack(out, f);
-                    uint8_t* half = static_cast<uint8_t*>(p.kc) + crow * kv4_row_bytes(D) +
-                                    (which == 2 ? kv4_half_bytes(D) : 0);
-                    kv4_store<IO, D>(half, f, c, store_kv);
+                    if (__any_sync(kFull, store_kv)) {
+                        ElemIO<IO>::unpack(out, f);
+                        uint8_t* half = static_cast<uint8_t*>(p.kc) + crow * kv4_row_bytes(D) +
+                                        (which == 2 ? kv4_half_bytes(D) : 0);
+                        kv4_store<IO, D>(half, f, c, store_kv);
+                    }
                 } else if constexpr (sizeof(KC) == 1) {
                     // int8 K: symmetric absmax over the row, codes rint(x * 127 / max|x|), ties to even.
                     float amax = 0.0f;
