@@ -134,19 +134,23 @@ template <int NG> __device__ __forceinline__ void load_words(const uint8_t* p, u
 }
 
 // The tiles of a block's share that fall to one warp, in order: tile i of the share
-// (counted over all its units) goes to warp i % NWARPS.
+// (counted over all its units) goes to warp i % NWARPS.  A share has fewer than 2^31 rows
+// (its rows are bytes of HBM): offsets into a unit's part of the share are 32 bits.
 template <int NWARPS, int TR>
 struct TileWalk {
     UnitWalk w;
     int64_t lo, hi, cap;   // the share; rows a unit may hold
-    int64_t r0, r1;        // the unit's rows in the share
-    int gt0, nt, k;        // share index of the unit's first tile, its tiles, this warp's next one
+    int64_t r0;            // first row of the unit's part of the share
+    int gt0, nt;           // share index of its first tile, its tiles
+    int at, left;          // this warp's tile: first row - r0, rows from there to the part's end
     __device__ __forceinline__ void unit(int warp) {
         const int64_t st = w.start();
         r0 = max(lo, st) - st;
-        r1 = min(min(hi, st + w.len()) - st, cap);
-        nt = r1 > r0 ? int((r1 - r0 + TR - 1) / TR) : 0;
-        k = (warp + NWARPS - gt0 % NWARPS) % NWARPS;
+        const int64_t r1 = min(min(hi, st + w.len()) - st, cap);
+        const int n = r1 > r0 ? int(r1 - r0) : 0;
+        nt = (n + TR - 1) / TR;
+        at = (warp + NWARPS - gt0 % NWARPS) % NWARPS * TR;
+        left = n - at;
     }
     __device__ __forceinline__ void begin(const int64_t* pre, int B, int Hkv, int64_t lo_, int64_t hi_, int64_t cap_,
                                           int warp) {
@@ -158,6 +162,10 @@ struct TileWalk {
         gt0 = 0;
         unit(warp);
     }
+    __device__ __forceinline__ void step() {
+        at += NWARPS * TR;
+        left -= NWARPS * TR;
+    }
     // the next unit of the share; false: there is none
     __device__ __forceinline__ bool next_unit(int warp) {
         if (!w.next() || w.start() >= hi) return false;
@@ -165,71 +173,99 @@ struct TileWalk {
         unit(warp);
         return true;
     }
-    // moves to a unit that still has a tile for this warp; false: the share is done
-    __device__ __forceinline__ bool settle(int warp) {
-        while (k >= nt)
-            if (!next_unit(warp)) return false;
-        return true;
-    }
-    __device__ __forceinline__ int64_t row() const { return r0 + int64_t(k) * TR; }
-    __device__ __forceinline__ int rows() const { return int(min(int64_t(TR), r1 - row())); }
 };
 
-// Fills `slot` with the walk's tile (the whole warp): the rows of each kv head of the
-// unit, one after the other.  Contiguous: one copy per kv head.  Paged: lane kv TR + i
-// finds the pool row of the tile's row i; the first row of each run of consecutive pool
-// rows copies the run.
-template <typename C, int KVH, bool PAGED, typename Walk>
-__device__ __forceinline__ void load_tile(const DecodeParams& p, const Walk& t, uint8_t* slot, uint64_t* bar,
-                                          uint64_t policy, int lane, bool* bad) {
-    const int n = t.rows();
-    const int b = t.w.b, g = t.w.g * KVH, heads = p.Hkv * KVH;
-    const uint8_t* rows = static_cast<const uint8_t*>(p.kc);
-    if constexpr (!PAGED) {
-        if (lane == 0) {
-            mbar_arrive_expect_tx(bar, uint32_t(KVH * n) * C::ROWB);
-#pragma unroll
-            for (int kv = 0; kv < KVH; ++kv)
-                bulk_copy_g2s(slot + kv * C::HEAD_BYTES,
-                              rows + ((int64_t(b) * heads + g + kv) * p.cap + t.row()) * C::ROWB,
-                              uint32_t(n) * C::ROWB, bar, policy);
-        }
-    } else {
-        const int64_t n_req = p.pos[b];
-        const int64_t Lk = n_req > 0 ? n_req + p.sink_len : 0;
-        const bool split = p.W > 0 && Lk > int64_t(p.S) + p.W;  // sinks, then the last W keys
-        const int i = lane % C::TR, kv = lane / C::TR;
-        const int64_t row = t.row() + i;
-        const int64_t key = split && row >= p.S ? Lk - p.W + (row - p.S) : row;
-        const bool active = i < n;
-        int64_t blk = 0;
-        if (active) {
-            if (key < p.sink_len) {
-                blk = p.sink_blocks[key >> p.bs_log2];
-            } else {
-                const int64_t j = (key - p.sink_len) >> p.bs_log2;
-                blk = j < p.max_blocks ? p.block_table[int64_t(b) * p.max_blocks + j] : -1;
-            }
-            if (blk < 0 || blk >= p.pool_blocks) {
-                *bad = true;
-                blk = 0;  // stay inside the pool; the error word reports it
-            }
-        }
-        const int64_t in = key & (p.bs - 1);
-        const bool first = active && (i == 0 || in == 0 || (split && row == p.S));
-        const uint32_t firsts = __ballot_sync(kFull, first);
-        if (lane == 0) mbar_arrive_expect_tx(bar, uint32_t(KVH * n) * C::ROWB);
-        __syncwarp();
-        if (first) {
-            // rows up to the next run of this kv head, or to the tile's end
-            const uint32_t later = (lane == 31 ? 0u : firsts >> (lane + 1)) & ((1u << (C::TR - 1 - i)) - 1u);
-            const int len = later != 0 ? __ffs(int(later)) : n - i;
-            bulk_copy_g2s(slot + kv * C::HEAD_BYTES + i * C::ROWB,
-                          rows + ((blk * heads + g + kv) * p.bs + in) * C::ROWB, uint32_t(len) * C::ROWB, bar,
-                          policy);
+// The loading side of a warp's walk: the current tile's source.
+template <typename C, int KVH, bool PAGED>
+struct Loader {
+    TileWalk<C::NWARPS, C::TR> t;
+    const uint8_t* src;   // contiguous: the tile's rows of the unit's first kv head
+    int64_t key0;         // paged: key of row r0 (at rows below `sinks_end`: the row itself)
+    int sinks_end;        // paged: offset from r0 at which the window's rows begin (at or before 0: all are)
+    bool more;
+    __device__ __forceinline__ void source(const DecodeParams& p) {
+        if constexpr (!PAGED) {
+            src = static_cast<const uint8_t*>(p.kc) +
+                  ((int64_t(t.w.b) * p.Hkv + t.w.g) * KVH * p.cap + t.r0 + t.at) * C::ROWB;
+        } else {
+            const int64_t n_req = p.pos[t.w.b];
+            const int64_t Lk = n_req > 0 ? n_req + p.sink_len : 0;
+            const bool split = p.W > 0 && Lk > int64_t(p.S) + p.W;  // sinks, then the last W keys
+            key0 = split ? Lk - p.W - p.S + t.r0 : t.r0;            // of a window row
+            sinks_end = split ? int(max(int64_t(-1), min(int64_t(p.S) - t.r0, int64_t(0x7fffffff)))) : -1;
         }
     }
-}
+    // moves on to a unit with a tile for this warp
+    __device__ __forceinline__ void settle(const DecodeParams& p, int warp) {
+        bool moved = false;
+        while (t.left <= 0) {
+            if (!t.next_unit(warp)) {
+                more = false;
+                return;
+            }
+            moved = true;
+        }
+        if (moved) source(p);
+    }
+    __device__ __forceinline__ void begin(const DecodeParams& p, int warp) {
+        more = true;
+        source(p);
+        settle(p, warp);
+    }
+    __device__ __forceinline__ void step(const DecodeParams& p, int warp) {
+        t.step();
+        if constexpr (!PAGED) src += C::NWARPS * C::HEAD_BYTES;
+        settle(p, warp);
+    }
+    // Fills `slot` with the tile (the whole warp): the rows of each kv head of the unit, one
+    // after the other.  Contiguous: one copy per kv head.  Paged: lane kv TR + i finds the
+    // pool row of the tile's row i; the first row of each run of consecutive pool rows
+    // copies the run.
+    __device__ __forceinline__ void load(const DecodeParams& p, uint8_t* slot, uint64_t* bar, uint64_t policy,
+                                         int lane, bool* bad) const {
+        const int n = min(t.left, C::TR);
+        if constexpr (!PAGED) {
+            if (lane == 0) {
+                mbar_arrive_expect_tx(bar, uint32_t(KVH * n) * C::ROWB);
+#pragma unroll
+                for (int kv = 0; kv < KVH; ++kv)
+                    bulk_copy_g2s(slot + kv * C::HEAD_BYTES, src + kv * p.cap * C::ROWB, uint32_t(n) * C::ROWB, bar,
+                                  policy);
+            }
+        } else {
+            const int i = lane % C::TR, kv = lane / C::TR, off = t.at + i;
+            const int64_t key = off < sinks_end ? t.r0 + off : key0 + off;
+            const bool active = i < n;
+            int64_t blk = 0;
+            if (active) {
+                if (key < p.sink_len) {
+                    blk = p.sink_blocks[key >> p.bs_log2];
+                } else {
+                    const int64_t j = (key - p.sink_len) >> p.bs_log2;
+                    blk = j < p.max_blocks ? p.block_table[int64_t(t.w.b) * p.max_blocks + j] : -1;
+                }
+                if (blk < 0 || blk >= p.pool_blocks) {
+                    *bad = true;
+                    blk = 0;  // stay inside the pool; the error word reports it
+                }
+            }
+            const int in = int(key) & (p.bs - 1);
+            const bool first = active && (i == 0 || in == 0 || off == sinks_end);
+            const uint32_t firsts = __ballot_sync(kFull, first);
+            if (lane == 0) mbar_arrive_expect_tx(bar, uint32_t(KVH * n) * C::ROWB);
+            __syncwarp();
+            if (first) {
+                // rows up to the next run of this kv head, or to the tile's end
+                const uint32_t later = (lane == 31 ? 0u : firsts >> (lane + 1)) & ((1u << (C::TR - 1 - i)) - 1u);
+                const int len = later != 0 ? __ffs(int(later)) : n - i;
+                const int64_t head = blk * (p.Hkv * KVH) + t.w.g * KVH + kv;
+                bulk_copy_g2s(slot + kv * C::HEAD_BYTES + i * C::ROWB,
+                              static_cast<const uint8_t*>(p.kc) + (head * p.bs + in) * C::ROWB,
+                              uint32_t(len) * C::ROWB, bar, policy);
+            }
+        }
+    }
+};
 
 // The online softmax state of one warp over a unit, for the lane's columns 2t, 2t + 1.
 template <int NG> struct State4 {
@@ -274,16 +310,16 @@ __global__ void __launch_bounds__(Cfg4<D, NREP, KVH>::THREADS, 1) decode4_split_
     const uint64_t policy = l2_policy_evict_first();
     bool timed_out = false, bad = false;
 
-    TileWalk<NWARPS, TR> ld, w;
+    TileWalk<NWARPS, TR> w;
     w.begin(pre, p.B, p.Hkv, lo, hi, cap, warp);
-    ld = w;
-    bool more = ld.settle(warp);
+    Loader<C, KVH, PAGED> ld;
+    ld.t = w;
+    ld.begin(p, warp);
     int slot = 0;
     uint32_t phase = 0;
-    for (int s = 0; s < SLOTS && more; ++s) {
-        load_tile<C, KVH, PAGED>(p, ld, ring + s * C::SLOT_BYTES, &bars[s], policy, lane, &bad);
-        ld.k += NWARPS;
-        more = ld.settle(warp);
+    for (int s = 0; s < SLOTS && ld.more; ++s) {
+        ld.load(p, ring + s * C::SLOT_BYTES, &bars[s], policy, lane, &bad);
+        ld.step(p, warp);
     }
 
     const uint32_t half_sel = (g8 & 1) ? 0x7632u : 0x5410u;  // which 4 codes of a word of 8 are this lane's
@@ -375,8 +411,8 @@ __global__ void __launch_bounds__(Cfg4<D, NREP, KVH>::THREADS, 1) decode4_split_
         st.limit = make_float2(-INFINITY, -INFINITY);
         st.vexp = kExpFloor;
 
-        for (; w.k < w.nt; w.k += NWARPS) {
-            const int n = w.rows();
+        for (; w.left > 0; w.step()) {
+            const int n = w.left;  // rows of the tile, if fewer than TR
             uint8_t* tile = ring + slot * C::SLOT_BYTES;
             if (!mbar_wait_bounded(&bars[slot], phase)) timed_out = true;
             if (n < TR) {  // rows past the tile's last one: zeros (whatever the slot held)
@@ -549,10 +585,9 @@ __global__ void __launch_bounds__(Cfg4<D, NREP, KVH>::THREADS, 1) decode4_split_
             // the slot has been read; zeros written to it come before the next copy
             if (n < TR) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            if (more) {
-                load_tile<C, KVH, PAGED>(p, ld, tile, &bars[slot], policy, lane, &bad);
-                ld.k += NWARPS;
-                more = ld.settle(warp);
+            if (ld.more) {
+                ld.load(p, tile, &bars[slot], policy, lane, &bad);
+                ld.step(p, warp);
             }
             if (++slot == SLOTS) { slot = 0; phase ^= 1; }
         }
