@@ -28,20 +28,32 @@
 // passes it by kSlack (a factor 2^8 of room), which in practice is once per unit: the
 // vote costs less than a reduction per tile.  Row sums are of the unrounded fp32 weights.
 //
-// Work split: as decode_kernels.cuh (the visible rows of all units end to end, an equal
-// share per block, partials combined by its combine kernels).  In a block each warp takes
-// 32-row tiles in turn and owns a ring of SLOTS tiles in shared memory that it fills with
-// bulk copies itself (one copy per tile, or per page): no producer, and no barrier
-// between warps until a unit ends and its warps' states are merged.
+// Work split: the visible rows of all units (a sequence and one or two kv heads) are laid
+// end to end and each block takes an equal share.  In a block each warp takes 32-row tiles
+// (16 rows of two kv heads) in turn and owns a ring of SLOTS tiles in shared memory that it
+// fills with bulk copies itself (one copy per tile and kv head, or per page): no producer,
+// and no barrier between warps until a unit ends and its warps' states are merged, each
+// through the ring slot that its warp has just emptied.
+//
+// One kernel: a block that holds all of a unit writes its output; a unit cut between blocks
+// is finished by whichever of them is last to write its partial (softmax states in the
+// workspace, added in the blocks' order, so the result does not depend on who is last).
+// The count of partials of a unit is a word of the workspace tagged with a number that is
+// this launch's own, so the workspace needs no initialisation: a word with another tag
+// counts as 0, and the last block writes it back to 0 (a graph replays its launch with the
+// same tag).  Nothing waits for another block.
 //
 // Rows are visited in an order that spreads a quarter warp's 16-byte loads over all
 // banks: matrix row r of a 16-row tile is key kappa(r), chosen so that (0,1), (2,3), ..
 // are 16 words apart mod 32 (K fragments) and so are (0,2,4,6) and (1,3,5,7) 8 apart (V).
 #include "decode4.cuh"
 
+#include <atomic>
+#include <chrono>
 #include <type_traits>
 
 #include <cuda_fp16.h>
+#include <unistd.h>
 
 #include "decode_kernels.cuh"
 #include "kv4.cuh"
@@ -55,9 +67,15 @@ constexpr float kSlack = 8.0f;      // a score may pass the reference by this mu
 constexpr int kExpFloor = -60;      // V scales below 2^-60 are taken as 2^-60 in the reference
 constexpr uint32_t kLowNibbles = 0x000F000Fu, kHighNibbles = 0x00F000F0u;
 
+// A unit of a block that other blocks share.
+struct Cut4 {
+    int64_t unit, first;  // the unit and the workspace slot of its first partial
+    int n, last;          // its partials; whether this block was the last to count one
+};
+
 // KVH kv heads share a block's unit: their q heads are columns 4 kv .. 4 kv + NREP - 1 of
 // the N side (KVH = 2, NREP <= 4) or 0 .. NREP - 1 (KVH = 1).
-template <int D, int NREP, int KVH> struct Cfg4 {
+template <typename T, int D, int NREP, int KVH> struct Cfg4 {
     static constexpr int NG = D / 32;                      // groups
     static constexpr int ROWB = kv4_row_bytes(D);
     static constexpr int HEADS = NREP * KVH;               // q heads of a unit
@@ -65,19 +83,23 @@ template <int D, int NREP, int KVH> struct Cfg4 {
     static constexpr int NWARPS = HEADS == 8 && KVH == 1 ? 8 : 12;
     static constexpr int HEAD_BYTES = TR * ROWB;           // a kv head's rows in a slot
     static constexpr int SLOT_BYTES = KVH * HEAD_BYTES;
-    static constexpr int MERGE_FLOATS = HEADS * (D + 2);   // per warp
-    // half of the warps' states at a time where all of them would not leave room for 3 slots
-    static constexpr int MERGE_ROUNDS = NWARPS * MERGE_FLOATS * 4 > 36 * 1024 ? 2 : 1;
-    static constexpr int MERGE_WARPS = NWARPS / MERGE_ROUNDS;
     static constexpr int SLOTS = NWARPS == 8 ? 4 : 3;
-    static constexpr size_t OFF_MERGE = size_t(NWARPS) * SLOTS * SLOT_BYTES;
-    static constexpr size_t OFF_PRE = OFF_MERGE + size_t(MERGE_WARPS) * MERGE_FLOATS * 4;
-    static constexpr size_t OFF_BAR = OFF_PRE + (kMaxBatch + 1) * 8;
-    static constexpr size_t SMEM = OFF_BAR + NWARPS * SLOTS * 8;
+    // a partial: the sums [HEADS][D], the references [HEADS], the sums of weights [HEADS]
+    static constexpr int PARTIAL_FLOATS = (HEADS * (D + 2) + 3) / 4 * 4;
+    static constexpr int Q_BYTES = HEADS * D * int(sizeof(T));   // a unit's q rows
+    static constexpr size_t OFF_Q = size_t(NWARPS) * SLOTS * SLOT_BYTES;
+    static constexpr size_t OFF_BAR = OFF_Q + 2 * Q_BYTES;       // slot barriers, then two of the q rows
+    static constexpr size_t OFF_ROWS = OFF_BAR + (NWARPS * SLOTS + 2) * 8;   // Rows4
+    static constexpr size_t OFF_M = (OFF_ROWS + (2 * kMaxBatch + 2) * 8 + 15) / 16 * 16;  // the warps' (m, l) per head
+    static constexpr size_t OFF_FLAGS = OFF_M + 2 * HEADS * NWARPS * 4;      // slot of each warp's sums
+    static constexpr size_t SMEM = OFF_FLAGS + NWARPS * 4 + 2 * sizeof(Cut4);
     static constexpr int THREADS = NWARPS * 32;
-    static constexpr int PARTIAL_FLOATS = HEADS * (D + 2);
+    static_assert(HEADS * D * 4 <= SLOT_BYTES, "a slot holds a warp's sums");
+    // workspace: a counter per unit, then the partials
+    __host__ __device__ static constexpr int64_t ws_counter_floats(int64_t units) { return (units + 1) / 2 * 4; }
     static_assert(KVH == 1 || (KVH == 2 && NREP <= 4), "columns");
-    static_assert(OFF_PRE % 8 == 0 && SMEM <= 232448, "shared memory");
+    static_assert(OFF_Q % 16 == 0 && OFF_BAR % 16 == 0 && OFF_M % 16 == 0 && NWARPS % 4 == 0, "alignment");
+    static_assert(SMEM <= 232448, "shared memory");
 };
 
 __device__ __forceinline__ int kappa(int r) { return (0x57463120 >> (4 * r)) & 7; }
@@ -133,43 +155,77 @@ template <int NG> __device__ __forceinline__ void load_words(const uint8_t* p, u
     }
 }
 
+__device__ __forceinline__ int64_t div_rows(int64_t a, int64_t b) {  // a, b >= 0
+    return ((a | b) >> 32) == 0 ? int64_t(uint32_t(a) / uint32_t(b)) : a / b;
+}
+
+// The rows of the batch in shared memory: len[b] visible rows of a unit of sequence b, and
+// start[b] = Hu * (len[0] + .. + len[b - 1]), the first row of its first unit; Hu units a
+// sequence.
+struct Rows4 {
+    int64_t* start;  // [B + 1]
+    int64_t* len;    // [B]
+};
+
+// The units of a share, in order.  A share has fewer than 2^31 rows (its rows are bytes of
+// HBM), so offsets into it are 32 bits.
+struct Units4 {
+    int b, g;     // sequence, unit of the sequence
+    int rows;     // the unit's rows in the share
+    int rest;     // the share's rows behind them
+    int64_t r0;   // the unit's first row in the share
+    __device__ __forceinline__ void begin(const Rows4& rw, int B, int64_t lo, int64_t hi) {
+        int l = 0, h = B;  // largest b with start[b] <= lo < start[b + 1]
+        while (h - l > 1) {
+            const int m = (l + h) >> 1;
+            if (rw.start[m] <= lo) l = m; else h = m;
+        }
+        b = l;
+        const int64_t len = rw.len[b], off = lo - rw.start[b];
+        g = int(div_rows(off, len));
+        r0 = off - g * len;
+        rest = int(hi - lo);
+        rows = int(min(int64_t(rest), len - r0));
+        rest -= rows;
+    }
+    // the next unit of the share; false: there is none
+    __device__ __forceinline__ bool next(const Rows4& rw, int Hu) {
+        if (rest == 0) return false;
+        if (++g == Hu) {
+            g = 0;
+            do { ++b; } while (rw.len[b] == 0);  // rows are left, so a sequence with rows is
+        }
+        r0 = 0;
+        rows = int(min(int64_t(rest), rw.len[b]));
+        rest -= rows;
+        return true;
+    }
+};
+
 // The tiles of a block's share that fall to one warp, in order: tile i of the share
-// (counted over all its units) goes to warp i % NWARPS.  A share has fewer than 2^31 rows
-// (its rows are bytes of HBM): offsets into a unit's part of the share are 32 bits.
+// (counted over all its units) goes to warp i % NWARPS.
 template <int NWARPS, int TR>
 struct TileWalk {
-    UnitWalk w;
-    int64_t lo, hi, cap;   // the share; rows a unit may hold
-    int64_t r0;            // first row of the unit's part of the share
-    int gt0, nt;           // share index of its first tile, its tiles
+    Units4 u;
+    int warp0;             // the warp that takes the unit's first tile
     int at, left;          // this warp's tile: first row - r0, rows from there to the part's end
     __device__ __forceinline__ void unit(int warp) {
-        const int64_t st = w.start();
-        r0 = max(lo, st) - st;
-        const int64_t r1 = min(min(hi, st + w.len()) - st, cap);
-        const int n = r1 > r0 ? int(r1 - r0) : 0;
-        nt = (n + TR - 1) / TR;
-        at = (warp + NWARPS - gt0 % NWARPS) % NWARPS * TR;
-        left = n - at;
+        at = (warp >= warp0 ? warp - warp0 : warp + NWARPS - warp0) * TR;
+        left = u.rows - at;
     }
-    __device__ __forceinline__ void begin(const int64_t* pre, int B, int Hkv, int64_t lo_, int64_t hi_, int64_t cap_,
-                                          int warp) {
-        w = UnitWalk{pre, B, Hkv, 0, 0};
-        w.seek(lo_);
-        lo = lo_;
-        hi = hi_;
-        cap = cap_;
-        gt0 = 0;
+    __device__ __forceinline__ void begin(const Rows4& rows, int B, int64_t lo, int64_t hi, int warp) {
+        u.begin(rows, B, lo, hi);
+        warp0 = 0;
         unit(warp);
     }
     __device__ __forceinline__ void step() {
         at += NWARPS * TR;
         left -= NWARPS * TR;
     }
-    // the next unit of the share; false: there is none
-    __device__ __forceinline__ bool next_unit(int warp) {
-        if (!w.next() || w.start() >= hi) return false;
-        gt0 += nt;
+    __device__ __forceinline__ bool next_unit(const Rows4& rows, int Hu, int warp) {
+        const int tiles = (u.rows + TR - 1) / TR;
+        if (!u.next(rows, Hu)) return false;
+        warp0 = (warp0 + tiles) % NWARPS;
         unit(warp);
         return true;
     }
@@ -186,20 +242,20 @@ struct Loader {
     __device__ __forceinline__ void source(const DecodeParams& p) {
         if constexpr (!PAGED) {
             src = static_cast<const uint8_t*>(p.kc) +
-                  ((int64_t(t.w.b) * p.Hkv + t.w.g) * KVH * p.cap + t.r0 + t.at) * C::ROWB;
+                  ((int64_t(t.u.b) * p.Hkv + t.u.g) * KVH * p.cap + t.u.r0 + t.at) * C::ROWB;
         } else {
-            const int64_t n_req = p.pos[t.w.b];
+            const int64_t n_req = p.pos[t.u.b];
             const int64_t Lk = n_req > 0 ? n_req + p.sink_len : 0;
             const bool split = p.W > 0 && Lk > int64_t(p.S) + p.W;  // sinks, then the last W keys
-            key0 = split ? Lk - p.W - p.S + t.r0 : t.r0;            // of a window row
-            sinks_end = split ? int(max(int64_t(-1), min(int64_t(p.S) - t.r0, int64_t(0x7fffffff)))) : -1;
+            key0 = split ? Lk - p.W - p.S + t.u.r0 : t.u.r0;            // of a window row
+            sinks_end = split ? int(max(int64_t(-1), min(int64_t(p.S) - t.u.r0, int64_t(0x7fffffff)))) : -1;
         }
     }
     // moves on to a unit with a tile for this warp
-    __device__ __forceinline__ void settle(const DecodeParams& p, int warp) {
+    __device__ __forceinline__ void settle(const DecodeParams& p, const Rows4& rows, int warp) {
         bool moved = false;
         while (t.left <= 0) {
-            if (!t.next_unit(warp)) {
+            if (!t.next_unit(rows, p.Hkv, warp)) {
                 more = false;
                 return;
             }
@@ -207,15 +263,15 @@ struct Loader {
         }
         if (moved) source(p);
     }
-    __device__ __forceinline__ void begin(const DecodeParams& p, int warp) {
+    __device__ __forceinline__ void begin(const DecodeParams& p, const Rows4& rows, int warp) {
         more = true;
         source(p);
-        settle(p, warp);
+        settle(p, rows, warp);
     }
-    __device__ __forceinline__ void step(const DecodeParams& p, int warp) {
+    __device__ __forceinline__ void step(const DecodeParams& p, const Rows4& rows, int warp) {
         t.step();
         if constexpr (!PAGED) src += C::NWARPS * C::HEAD_BYTES;
-        settle(p, warp);
+        settle(p, rows, warp);
     }
     // Fills `slot` with the tile (the whole warp): the rows of each kv head of the unit, one
     // after the other.  Contiguous: one copy per kv head.  Paged: lane kv TR + i finds the
@@ -234,7 +290,7 @@ struct Loader {
             }
         } else {
             const int i = lane % C::TR, kv = lane / C::TR, off = t.at + i;
-            const int64_t key = off < sinks_end ? t.r0 + off : key0 + off;
+            const int64_t key = off < sinks_end ? t.u.r0 + off : key0 + off;
             const bool active = i < n;
             int64_t blk = 0;
             if (active) {
@@ -242,7 +298,7 @@ struct Loader {
                     blk = p.sink_blocks[key >> p.bs_log2];
                 } else {
                     const int64_t j = (key - p.sink_len) >> p.bs_log2;
-                    blk = j < p.max_blocks ? p.block_table[int64_t(t.w.b) * p.max_blocks + j] : -1;
+                    blk = j < p.max_blocks ? p.block_table[int64_t(t.u.b) * p.max_blocks + j] : -1;
                 }
                 if (blk < 0 || blk >= p.pool_blocks) {
                     *bad = true;
@@ -258,7 +314,7 @@ struct Loader {
                 // rows up to the next run of this kv head, or to the tile's end
                 const uint32_t later = (lane == 31 ? 0u : firsts >> (lane + 1)) & ((1u << (C::TR - 1 - i)) - 1u);
                 const int len = later != 0 ? __ffs(int(later)) : n - i;
-                const int64_t head = blk * (p.Hkv * KVH) + t.w.g * KVH + kv;
+                const int64_t head = blk * (p.Hkv * KVH) + t.u.g * KVH + kv;
                 bulk_copy_g2s(slot + kv * C::HEAD_BYTES + i * C::ROWB,
                               static_cast<const uint8_t*>(p.kc) + (head * p.bs + in) * C::ROWB,
                               uint32_t(len) * C::ROWB, bar, policy);
@@ -277,49 +333,207 @@ template <int NG> struct State4 {
     int vexp;             // exponent of the V scale in the reference (the same in all lanes)
 };
 
+// Output of 4 dims of a unit's head h: weighted sums a and the sum of weights l at reference
+// M (both in 2^(score - M)), and the learned sink, one more logit of the denominator.
+template <typename T, int D, int HEADS>
+__device__ __forceinline__ void finish(const DecodeParams& p, int64_t unit, int h, int dim, float M, float l,
+                                       const float4& a) {
+    const int Hq = p.Hkv * HEADS;
+    float f = 1.0f;
+    if (p.sink_logits != nullptr) {
+        const float z = fminf(fmaxf(p.sink_logits[int(unit % p.Hkv) * HEADS + h], kSinkLogitMin), kSinkLogitMax) *
+                        kLog2e;
+        const float top = fmaxf(M, z);
+        f = fast_exp2_approx(M - top);
+        l = l * f + fast_exp2_approx(z - top);
+    }
+    const float inv = l > 0.0f ? f / l : (l == l ? 0.0f : l);  // NaN stays
+    T* o = static_cast<T*>(p.out) + (unit / p.Hkv * Hq + unit % p.Hkv * HEADS + h) * D + dim;
+    const float v[4] = {a.x * inv, a.y * inv, a.z * inv, a.w * inv};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (std::is_same<T, float>::value) o[i] = v[i];
+        else o[i] = __float2bfloat16_rn(v[i]);
+    }
+}
+
+// The output of a unit from its n partials, `first` on, added in their order (the block).
+// w: room for 2 (n + 1) HEADS floats of shared memory.
+template <typename T, int D, int HEADS, int PF, int THREADS>
+__device__ __noinline__ void combine_unit(const DecodeParams& p, int64_t unit, const float* first, int n,
+                                             float* w) {
+    float* ls = w + n * HEADS;        // [n][HEADS] sums of weights
+    float* top = ls + n * HEADS;      // [HEADS] reference, then the sum of weights
+    for (int i = threadIdx.x; i < n * HEADS; i += THREADS) {
+        const float* part = first + int64_t(i / HEADS) * PF + HEADS * D + i % HEADS;
+        w[i] = __ldcg(part);
+        ls[i] = __ldcg(part + HEADS);
+    }
+    __syncthreads();
+    if (threadIdx.x < HEADS) {
+        float M = -INFINITY, l = 0.0f;
+        for (int i = 0; i < n; ++i) M = fmaxf(M, w[i * HEADS + threadIdx.x]);
+        for (int i = 0; i < n; ++i) {
+            const float f = fast_exp2_approx(w[i * HEADS + threadIdx.x] - M);
+            w[i * HEADS + threadIdx.x] = f;
+            l = fmaf(ls[i * HEADS + threadIdx.x], f, l);
+        }
+        top[threadIdx.x] = M;
+        top[HEADS + threadIdx.x] = l;
+    }
+    __syncthreads();
+    for (int idx = threadIdx.x; idx < HEADS * D / 4; idx += THREADS) {
+        const int h = idx / (D / 4);
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+        const float* part = first + idx * 4;
+        constexpr int U = 8;  // partials in flight
+#pragma unroll 1
+        for (int i0 = 0; i0 < n; i0 += U) {
+            float4 v[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (i0 + u < n) v[u] = __ldcg(reinterpret_cast<const float4*>(part + int64_t(i0 + u) * PF));
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (i0 + u >= n) break;
+                const float f = w[(i0 + u) * HEADS + h];
+                a.x = fmaf(v[u].x, f, a.x);
+                a.y = fmaf(v[u].y, f, a.y);
+                a.z = fmaf(v[u].z, f, a.z);
+                a.w = fmaf(v[u].w, f, a.w);
+            }
+        }
+        finish<T, D, HEADS>(p, unit, h, idx % (D / 4) * 4, top[h], top[HEADS + h], a);
+    }
+    __syncthreads();
+}
+
+// Counts one of a unit's n partials; true for the last.  The word holds the launch's tag
+// (48 bits) and the count.
+__device__ __forceinline__ bool count_partial(unsigned long long* word, uint64_t tag, int n) {
+    unsigned long long seen = 0;  // as a finished call leaves it
+    while (true) {
+        const unsigned long long now = (seen >> 16) == tag ? seen + 1 : ((tag << 16) | 1ull);
+        const bool all = int(now & 0xFFFF) == n;
+        const unsigned long long was = atomicCAS(word, seen, all ? 0ull : now);
+        if (was == seen) return all;
+        seen = was;
+    }
+}
+
 template <typename T, int D, int NREP, int KVH, bool PAGED>
-__global__ void __launch_bounds__(Cfg4<D, NREP, KVH>::THREADS, 1) decode4_split_kernel(DecodeParams p) {
-    using C = Cfg4<D, NREP, KVH>;
+__global__ void __launch_bounds__(Cfg4<T, D, NREP, KVH>::THREADS, 1) decode4_kernel(DecodeParams p, uint64_t tag) {
+    using C = Cfg4<T, D, NREP, KVH>;
     constexpr int NG = C::NG, NWARPS = C::NWARPS, SLOTS = C::SLOTS, TR = C::TR, HEADS = C::HEADS;
     constexpr bool F32 = std::is_same<T, float>::value;
     static_assert(!F32 || KVH == 1, "fp32 calls: registers for one kv head's q");
     constexpr int NQ = F32 ? 2 : 1;          // fp16 parts of q and of P'
     constexpr int NM = KVH == 1 ? 2 : 1;     // 16-row matrix tiles of scores
     extern __shared__ __align__(128) uint8_t smem[];
-    float* merge = reinterpret_cast<float*>(smem + C::OFF_MERGE);
-    int64_t* pre = reinterpret_cast<int64_t*>(smem + C::OFF_PRE);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g8 = lane >> 2, t4 = lane & 3;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR) + warp * SLOTS;
+    uint64_t* all_bars = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+    uint64_t* bars = all_bars + warp * SLOTS;
+    uint64_t* q_bars = all_bars + NWARPS * SLOTS;
     uint8_t* ring = smem + size_t(warp) * SLOTS * C::SLOT_BYTES;
+    const Rows4 rows{reinterpret_cast<int64_t*>(smem + C::OFF_ROWS),
+                     reinterpret_cast<int64_t*>(smem + C::OFF_ROWS) + kMaxBatch + 1};
+    float* warp_m = reinterpret_cast<float*>(smem + C::OFF_M);  // [HEADS][NWARPS] references
+    float* warp_l = warp_m + HEADS * NWARPS;                    // [HEADS][NWARPS] sums, at the block's reference
+    int* warp_slot = reinterpret_cast<int*>(smem + C::OFF_FLAGS);  // [NWARPS] where a warp's sums are; -1: none
+    Cut4* cuts = reinterpret_cast<Cut4*>(warp_slot + NWARPS);      // [2]
     pdl_trigger();
     if (lane == 0) {
         for (int s = 0; s < SLOTS; ++s) mbar_init(&bars[s], 1);
+        if (warp == 0) {
+            mbar_init(&q_bars[0], 1);
+            mbar_init(&q_bars[1], 1);
+        }
         fence_barrier_init();
     }
-    pdl_wait();  // the append before this kernel has written the state, q and the new rows
-    if (warp == 0) unit_prefix(p, pre, lane);
-    __syncthreads();
-
-    const int P = gridDim.x, c = blockIdx.x;
-    const int64_t R = pre[p.B];
-    const int64_t lo = (int64_t(c) * R + P - 1) / P;
-    const int64_t hi = (int64_t(c + 1) * R + P - 1) / P;
-    if (R == 0 || lo >= hi) return;
-    const int64_t cap = PAGED ? (int64_t(1) << 62) : p.cap;
+    // The split of the batch is worked out twice at most: from the state as it reads before
+    // the wait, while the kernel ahead (an append, another layer) still runs, and again after
+    // it where a length has changed by then (a full ring's does not).
     const uint64_t policy = l2_policy_evict_first();
+    const int64_t units = int64_t(p.B) * p.Hkv;
+    const int c = blockIdx.x;
     bool timed_out = false, bad = false;
-
+    int64_t R = 0;
+    int P = 0;
     TileWalk<NWARPS, TR> w;
-    w.begin(pre, p.B, p.Hkv, lo, hi, cap, warp);
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+        if (pass == 1) pdl_wait();  // the append has written the state, q and the new rows
+        bool changed = false;
+        for (int b = threadIdx.x; b < p.B; b += C::THREADS) {
+            int64_t n = visible_rows(p, b);
+            n = max(int64_t(0), PAGED ? n : min(n, p.cap));
+            if (pass == 0 || rows.len[b] != n) {
+                rows.len[b] = n;
+                changed = true;
+            }
+        }
+        if (!__syncthreads_or(changed)) break;
+        if (warp == 0) {  // scan
+            int64_t carry = 0;
+            for (int b0 = 0; b0 < p.B; b0 += 32) {
+                const int b = b0 + lane;
+                int64_t x = b < p.B ? p.Hkv * rows.len[b] : 0;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int64_t y = __shfl_up_sync(kFull, x, o);
+                    if (lane >= o) x += y;
+                }
+                if (b < p.B) rows.start[b + 1] = carry + x;
+                carry += __shfl_sync(kFull, x, 31);
+            }
+            if (lane == 0) rows.start[0] = 0;
+        }
+        __syncthreads();
+        // Blocks that take part: enough for one tile a warp, or one unit each if that is more
+        // (every block of them has a row).
+        R = rows.start[p.B];
+        P = int(min(int64_t(gridDim.x), max(min(units, R), R / (NWARPS * TR))));
+        // Units of one length that nearly fill the GPU: one to a block, nothing is cut (measured on
+        // 128 units of 4096 rows over 152 SMs: 41.4 -> 36.7 us, the stream alone the same).
+        if (units <= gridDim.x && units * 4 >= int64_t(gridDim.x) * 3 && R == units * rows.len[0]) P = int(units);
+        if (c < P) {
+            w.begin(rows, p.B, div_rows(int64_t(c) * R + P - 1, P), div_rows(int64_t(c + 1) * R + P - 1, P), warp);
+        }
+    }
+
+    // sequences with nothing visible: zeros, each from one block
+    for (int b = blockIdx.x; b < p.B; b += gridDim.x)
+        if (rows.len[b] == 0)
+            for (int i = threadIdx.x; i < p.Hkv * HEADS * D; i += C::THREADS)
+                static_cast<T*>(p.out)[int64_t(b) * p.Hkv * HEADS * D + i] = T(0.0f);
+    if (c >= P) return;  // R = 0 too
+    // q rows of the share's units, two units ahead, into two slots (one thread)
+    Units4 qu = w.u;
+    bool q_more = true;
+    auto load_q = [&](int qs) {
+        mbar_arrive_expect_tx(&q_bars[qs], C::Q_BYTES);
+        bulk_copy_g2s_nohint(smem + C::OFF_Q + qs * C::Q_BYTES,
+                             static_cast<const T*>(p.q) + (int64_t(qu.b) * p.Hkv + qu.g) * (HEADS * D), C::Q_BYTES,
+                             &q_bars[qs]);
+        q_more = qu.next(rows, p.Hkv);
+    };
+    if (threadIdx.x == 0) {
+        load_q(0);
+        if (q_more) load_q(1);
+    }
+    int q_at = 0;
+    uint32_t q_phase = 0;
+    float* partials = p.ws + C::ws_counter_floats(units);
+    int n_cuts = 0;
     Loader<C, KVH, PAGED> ld;
     ld.t = w;
-    ld.begin(p, warp);
+    ld.begin(p, rows, warp);
     int slot = 0;
     uint32_t phase = 0;
     for (int s = 0; s < SLOTS && ld.more; ++s) {
         ld.load(p, ring + s * C::SLOT_BYTES, &bars[s], policy, lane, &bad);
-        ld.step(p, warp);
+        ld.step(p, rows, warp);
     }
 
     const uint32_t half_sel = (g8 & 1) ? 0x7632u : 0x5410u;  // which 4 codes of a word of 8 are this lane's
@@ -335,8 +549,7 @@ __global__ void __launch_bounds__(Cfg4<D, NREP, KVH>::THREADS, 1) decode4_split_
     const __half2 keep[2] = {__float2half2_rn(KVH == 1 || g8 < 4 ? 1.0f : 0.0f),
                              __float2half2_rn(g8 < 4 ? 0.0f : 1.0f)};
     do {
-        const int b = w.w.b, g = w.w.g;
-        const int64_t unit = int64_t(b) * p.Hkv + g;
+        const int64_t unit = int64_t(w.u.b) * p.Hkv + w.u.g;
         // ---- q as the N-side operand: column g8, dims 32 grp + 8 t4 .. + 7 ----
         uint32_t qb[KVH][NQ][NG][4];
         float fac;  // score units (log2) per accumulator unit, of column g8
@@ -345,7 +558,8 @@ __global__ void __launch_bounds__(Cfg4<D, NREP, KVH>::THREADS, 1) decode4_split_
             const bool real = KVH == 1 ? g8 < NREP : (g8 & 3) < NREP;
             float qf[NG][8];
             float amax = 0.0f;
-            const T* qrow = static_cast<const T*>(p.q) + (unit * HEADS + qh) * D;
+            const T* qrow = reinterpret_cast<const T*>(smem + C::OFF_Q + q_at * C::Q_BYTES) + qh * D;
+            if (!mbar_wait_bounded(&q_bars[q_at], q_phase)) timed_out = true;
 #pragma unroll
             for (int r = 0; r < NG; ++r) {
                 constexpr int V = ElemIO<T>::kPerVec;
@@ -411,6 +625,7 @@ __global__ void __launch_bounds__(Cfg4<D, NREP, KVH>::THREADS, 1) decode4_split_
         st.limit = make_float2(-INFINITY, -INFINITY);
         st.vexp = kExpFloor;
 
+        int last = -1;  // the slot of the warp's last tile of the unit
         for (; w.left > 0; w.step()) {
             const int n = w.left;  // rows of the tile, if fewer than TR
             uint8_t* tile = ring + slot * C::SLOT_BYTES;
@@ -582,17 +797,19 @@ __global__ void __launch_bounds__(Cfg4<D, NREP, KVH>::THREADS, 1) decode4_split_
                     }
                 }
             }
-            // the slot has been read; zeros written to it come before the next copy
+            // the slot has been read; zeros written to it come before the next copy.  The slot
+            // of the warp's last tile of the unit is refilled after the merge, which uses it.
             if (n < TR) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            if (ld.more) {
+            if (ld.more && n > NWARPS * TR) {
                 ld.load(p, tile, &bars[slot], policy, lane, &bad);
-                ld.step(p, warp);
+                ld.step(p, rows, warp);
             }
+            last = slot;
             if (++slot == SLOTS) { slot = 0; phase ^= 1; }
         }
 
-        // ---- merge the warps' states and write this block's partial of the unit ----
+        // ---- merge the warps' states ----
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) {
             st.l.x += __shfl_xor_sync(kFull, st.l.x, o);
@@ -603,103 +820,142 @@ __global__ void __launch_bounds__(Cfg4<D, NREP, KVH>::THREADS, 1) decode4_split_
                 st.om[r].y += __shfl_xor_sync(kFull, st.om[r].y, o);
             }
         }
-        float* outp = p.ws + (unit + c) * C::PARTIAL_FLOATS;
+        // column 2 t4 + e is head h_of(e) of the unit, if it is one
+        auto h_of = [&](int e) { return KVH == 1 ? 2 * t4 + e : (t4 >> 1) * NREP + ((2 * t4 + e) & 3); };
+        auto is_head = [&](int e) { return KVH == 1 ? 2 * t4 + e < NREP : ((2 * t4 + e) & 3) < NREP; };
         const float mshift = float(st.vexp - kHead);
-        constexpr int PER = (HEADS * D + C::THREADS - 1) / C::THREADS;  // values of the partial per thread
-        float acc[PER], accM[PER], accL[PER];
+        const float m_own[2] = {last < 0 ? -INFINITY : st.ref.x + mshift, last < 0 ? -INFINITY : st.ref.y + mshift};
+        if (g8 == 0) {
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            acc[i] = accL[i] = 0.0f;
-            accM[i] = -INFINITY;
+            for (int e = 0; e < 2; ++e)
+                if (is_head(e)) warp_m[h_of(e) * NWARPS + warp] = m_own[e];
         }
-        for (int round = 0; round < C::MERGE_ROUNDS; ++round) {
-            if (warp / C::MERGE_WARPS == round) {
-                float* mw = merge + (warp % C::MERGE_WARPS) * C::MERGE_FLOATS;
+        if (lane == 0) warp_slot[warp] = last;
+        __syncthreads();
+        {
+            float* sums = reinterpret_cast<float*>(ring + max(last, 0) * C::SLOT_BYTES);  // [HEADS][D]
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int col = 2 * t4 + e;
-                    const int h = KVH == 1 ? col : (col >> 2) * NREP + (col & 3);
-                    if (KVH == 1 ? col < NREP : (col & 3) < NREP) {
-                        if (g8 == 0) {
-                            const float ref = e ? st.ref.y : st.ref.x;
-                            mw[h] = ref == kRefNone ? -INFINITY : ref + mshift;
-                            mw[HEADS + h] = e ? st.l.y : st.l.x;
-                        }
+            for (int e = 0; e < 2; ++e) {
+                if (!is_head(e)) continue;
+                const int h = h_of(e);
+                const float4* ms = reinterpret_cast<const float4*>(warp_m + h * NWARPS);
+                float M = -INFINITY;
 #pragma unroll
-                        for (int r = 0; r < NG; ++r) {
-                            const float m = e ? st.om[r].y : st.om[r].x;
-                            float4 v;
-                            v.x = fmaf(st.o[r][0][e], 16777216.0f, m);        // 2^24: even nibbles
-                            v.y = fmaf(st.o[r][0][2 + e], 1048576.0f, m);     // 2^20: odd nibbles
-                            v.z = fmaf(st.o[r][1][e], 16777216.0f, m);
-                            v.w = fmaf(st.o[r][1][2 + e], 1048576.0f, m);
-                            float* d = mw + 2 * HEADS + h * D + 32 * r + 4 * g8;
-                            reinterpret_cast<float2*>(d)[0] = make_float2(v.x, v.y);
-                            reinterpret_cast<float2*>(d)[1] = make_float2(v.z, v.w);
-                        }
-                    }
+                for (int i = 0; i < NWARPS / 4; ++i)
+                    M = fmaxf(fmaxf(M, fmaxf(ms[i].x, ms[i].y)), fmaxf(ms[i].z, ms[i].w));
+                const float f = last < 0 ? 0.0f : fast_exp2_approx(m_own[e] - M);  // M >= m_own > -inf
+                const float f24 = f * 16777216.0f, f20 = f * 1048576.0f;           // even / odd nibbles
+                if (g8 == 0) warp_l[h * NWARPS + warp] = last < 0 ? 0.0f : (e ? st.l.y : st.l.x) * f;
+                if (last < 0) continue;  // the slots hold tiles of the next unit
+#pragma unroll
+                for (int r = 0; r < NG; ++r) {
+                    const float m = (e ? st.om[r].y : st.om[r].x) * f;
+                    *reinterpret_cast<float4*>(sums + h * D + 32 * r + 4 * g8) =
+                        make_float4(fmaf(st.o[r][0][e], f24, m), fmaf(st.o[r][0][2 + e], f20, m),
+                                    fmaf(st.o[r][1][e], f24, m), fmaf(st.o[r][1][2 + e], f20, m));
                 }
             }
-            __syncthreads();
+        }
+        __syncthreads();
+        const bool whole = w.u.rows == rows.len[w.u.b];
+        float* part = partials + (unit + c) * C::PARTIAL_FLOATS;
+        for (int idx = threadIdx.x; idx < HEADS * D / 4; idx += C::THREADS) {
+            const int h = idx / (D / 4);
+            const float4* ms = reinterpret_cast<const float4*>(warp_m + h * NWARPS);
+            const float4* ls = reinterpret_cast<const float4*>(warp_l + h * NWARPS);
+            float M = -INFINITY, l = 0.0f;
+            float4 v[NWARPS];
 #pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const int idx = threadIdx.x + i * C::THREADS;
-                if (idx >= HEADS * D) break;
-                const int h = idx / D;
-                float M = accM[i];
+            for (int ww = 0; ww < NWARPS; ++ww) {
+                const int at = warp_slot[ww];
+                v[ww] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (at >= 0)
+                    v[ww] = reinterpret_cast<const float4*>(smem + (ww * SLOTS + at) * C::SLOT_BYTES)[idx];
+            }
+            float4 a = v[0];
 #pragma unroll
-                for (int ww = 0; ww < C::MERGE_WARPS; ++ww) M = fmaxf(M, merge[ww * C::MERGE_FLOATS + h]);
-                const float Mu = M == -INFINITY ? 0.0f : M;
-                const float f0 = fast_exp2_approx(accM[i] - Mu);
-                float a = acc[i] * f0, lsum = accL[i] * f0;
+            for (int ww = 1; ww < NWARPS; ++ww)
+                a = make_float4(a.x + v[ww].x, a.y + v[ww].y, a.z + v[ww].z, a.w + v[ww].w);
 #pragma unroll
-                for (int ww = 0; ww < C::MERGE_WARPS; ++ww) {
-                    const float* mm = merge + ww * C::MERGE_FLOATS;
-                    const float f = fast_exp2_approx(mm[h] - Mu);
-                    a = fmaf(f, mm[2 * HEADS + idx], a);
-                    lsum = fmaf(f, mm[HEADS + h], lsum);
+            for (int i = 0; i < NWARPS / 4; ++i) {
+                M = fmaxf(fmaxf(M, fmaxf(ms[i].x, ms[i].y)), fmaxf(ms[i].z, ms[i].w));
+                l += (ls[i].x + ls[i].y) + (ls[i].z + ls[i].w);
+            }
+            if (whole) {
+                finish<T, D, HEADS>(p, unit, h, idx % (D / 4) * 4, M, l, a);
+            } else {
+                reinterpret_cast<float4*>(part)[idx] = a;
+                if (idx % (D / 4) == 0) {
+                    part[HEADS * D + h] = M;
+                    part[HEADS * (D + 1) + h] = l;
                 }
-                acc[i] = a;
-                accL[i] = lsum;
-                accM[i] = M;
-            }
-            __syncthreads();
-        }
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int idx = threadIdx.x + i * C::THREADS;
-            if (idx >= HEADS * D) break;
-            outp[2 * HEADS + idx] = acc[i];
-            if (idx % D == 0) {
-                outp[idx / D] = accM[i];
-                outp[HEADS + idx / D] = accL[i];
             }
         }
-    } while (w.next_unit(warp));
+        if (!whole) {  // a share has two cut units at most: its first and its last
+            if (threadIdx.x == 0) {
+                const int64_t len = rows.len[w.u.b], start = rows.start[w.u.b] + w.u.g * len;
+                const int64_t from = div_rows(start * P, R);  // the unit's blocks: from, from + 1, ..
+                cuts[n_cuts].unit = unit;
+                cuts[n_cuts].first = unit + from;
+                cuts[n_cuts].n = int(div_rows((start + len - 1) * P, R) - from) + 1;
+            }
+            ++n_cuts;
+        }
+        // sums were written to the slots the ordinary way; bulk copies come next
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncthreads();
+        if (last >= 0 && ld.more) {
+            ld.load(p, ring + last * C::SLOT_BYTES, &bars[last], policy, lane, &bad);
+            ld.step(p, rows, warp);
+        }
+        if (threadIdx.x == 0 && q_more) load_q(q_at);
+        if (++q_at == 2) { q_at = 0; q_phase ^= 1; }
+    } while (w.next_unit(rows, p.Hkv, warp));
+
+    // ---- the cut units: count this block's partials, and finish the units that are now whole ----
+    if (n_cuts > 0) {
+        __threadfence();  // the partials are visible before they are counted
+        __syncthreads();
+        if (threadIdx.x < n_cuts) {
+            Cut4& cut = cuts[threadIdx.x];
+            cut.last = count_partial(reinterpret_cast<unsigned long long*>(p.ws) + cut.unit, tag, cut.n) ? 1 : 0;
+        }
+        __syncthreads();
+        __threadfence();
+        // the ring is empty: its first bytes hold the weights of the partials
+#pragma unroll 1
+        for (int i = 0; i < n_cuts; ++i) {
+            const Cut4 cut = cuts[i];
+            if (cut.last)
+                combine_unit<T, D, HEADS, C::PARTIAL_FLOATS, C::THREADS>(
+                    p, cut.unit, partials + cut.first * C::PARTIAL_FLOATS, cut.n, reinterpret_cast<float*>(smem));
+        }
+    }
     if (timed_out) set_error(p.err, SK_DEVERR_TIMEOUT);
     if (bad) set_error(p.err, SK_DEVERR_BLOCK_TABLE);
 }
 
+// A 48-bit number that no other launch of this process has, from a random start.
+uint64_t launch_tag() {
+    static std::atomic<uint64_t> next{[] {
+        uint64_t x = uint64_t(std::chrono::system_clock::now().time_since_epoch().count()) ^ (uint64_t(getpid()) << 40);
+        x = (x ^ (x >> 30)) * 0xBF58476D1CE4E5B9ull;
+        return x ^ (x >> 27);
+    }()};
+    return next.fetch_add(1, std::memory_order_relaxed) & 0xFFFFFFFFFFFFull;
+}
+
 template <typename T, int D, int NREP, int KVH, bool PAGED>
 cudaError_t run4(DecodeParams p, int64_t rows_most, cudaStream_t st) {
-    using C = Cfg4<D, NREP, KVH>;
-    constexpr int HEADS = C::HEADS;
+    using C = Cfg4<T, D, NREP, KVH>;
     static PerDevice<cudaError_t> attr;
-    const cudaError_t a = set_smem_limit_once(attr, decode4_split_kernel<T, D, NREP, KVH, PAGED>, int(C::SMEM));
+    const cudaError_t a = set_smem_limit_once(attr, decode4_kernel<T, D, NREP, KVH, PAGED>, int(C::SMEM));
     if (a != cudaSuccess) return a;
-    p.Hkv /= KVH;  // units of KVH kv heads, HEADS q heads each, for both kernels
-    const int64_t units = int64_t(p.B) * p.Hkv;
-    // no more blocks than rows the cache can hold: they would only add partials to skip
+    p.Hkv /= KVH;  // units of KVH kv heads
+    // no more blocks than rows the cache can hold
     p.n_blocks = int(std::max<int64_t>(1, std::min<int64_t>(device_sm_count(), rows_most / KVH)));
-    cudaError_t e = launch_pdl(decode4_split_kernel<T, D, NREP, KVH, PAGED>, dim3(p.n_blocks), dim3(C::THREADS),
-                               C::SMEM, st, p);
-    if (e != cudaSuccess) return e;
-    p.combine_wpu = combine_wpu(p.n_blocks, units);
-    const int64_t warps = units * HEADS * p.combine_wpu;
-    return p.combine_wpu == 1
-               ? launch_pdl(decode_combine_kernel<T, D, HEADS>, dim3(unsigned((warps + 7) / 8)), dim3(256), 0, st, p)
-               : launch_pdl(decode_combine_group_kernel<T, D, HEADS>, dim3(unsigned((warps + 7) / 8)), dim3(256), 0,
-                            st, p);
+    return launch_pdl(decode4_kernel<T, D, NREP, KVH, PAGED>, dim3(p.n_blocks), dim3(C::THREADS), C::SMEM, st, p,
+                      launch_tag());
 }
 
 template <typename T, int D>
@@ -733,9 +989,12 @@ bool dispatch4(int nrep, const DecodeParams& p, int64_t rows_most, cudaStream_t 
 
 size_t kv4_decode_workspace(int batch, int n_kv_heads, int head_dim, int nrep) {
     if ((head_dim != 64 && head_dim != 128) || (nrep != 1 && nrep != 2 && nrep != 4 && nrep != 8)) return 0;
-    // a slot per block and unit; a unit has the q heads of up to two kv heads
+    // a counter per unit; a partial per block and unit, of the q heads of up to two kv heads
     const int pair = nrep <= 4 && n_kv_heads % 2 == 0 ? 2 : 1;
-    return size_t(int64_t(device_sm_count()) * pair + int64_t(batch) * n_kv_heads) * nrep * (head_dim + 2) *
+    const int64_t units = int64_t(batch) * n_kv_heads;
+    const int64_t heads = int64_t(nrep) * pair;
+    return size_t((units / pair + 1) / 2 * 4 +
+                  (device_sm_count() + units / pair) * ((heads * (head_dim + 2) + 3) / 4 * 4)) *
            sizeof(float);
 }
 
