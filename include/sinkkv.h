@@ -134,7 +134,8 @@ typedef struct {
  * PagedAttention: a shared pool of fixed-size blocks and a per-request block table
  * from logical block to physical block; [RoPE] "Hybrid models break the uniform-spec
  * assumption": static sink blocks put in front of every block table).  All pointers
- * are device pointers owned by the caller; the caller allocates and frees blocks.
+ * are device pointers owned by the caller; the caller allocates and frees blocks, itself
+ * or with sk_paged_reserve / fork / compact.
  *   k_pool, v_pool: [n_blocks][n_kv_heads][block_size][head_dim] of k_dtype / v_dtype
  *   block_table: int32 [batch][max_blocks]; request block j holds the request's tokens
  *     [j*block_size, (j+1)*block_size).  Entries of blocks that hold no visible key may
@@ -506,6 +507,69 @@ SK_API size_t sk_paged_decode_workspace_bytes(const sk_paged_layer* layer, int32
 SK_API sk_status sk_paged_decode_attention(const sk_paged_layer* layer, const void* q_rot, int32_t n_q_heads,
                                            int32_t io_dtype, const float* sink_logits, void* out,
                                            void* workspace, size_t ws_bytes, void* stream);
+
+/* ---- Pages: reserving, forking and compacting the blocks of paged layers --------------- */
+
+/* The calls below manage the blocks of one block table for all layers that share it:
+ * `layers` (host array of n_layers <= 128 descriptors) agree in block_table, batch (<= 1024),
+ * max_blocks, block_size, n_blocks, sinks, window and static sink blocks; each has its own
+ * pools, and its own seq_lens or a shared one.  The table is written (the descriptor's const
+ * is the attention's view of it).
+ *   ref: device int32 [n_blocks], caller-owned: how many table entries name each block, plus
+ *     the caller's own holds (static sink blocks need one of their own); 0 is a free block.
+ *     The calls keep it so.  Zeros (and -1 in every table entry) start an empty pool.
+ * All decisions are taken on the device, in the order of requests, table entries and block
+ * ids, so the same state always gives the same result; nothing is copied to the host.
+ * Device conditions set a bit in layers[0].err.
+ *
+ * Workspace bytes of sk_paged_reserve and sk_paged_compact for layers like `layer`
+ * (0: not supported).  16-byte aligned, no initialisation; its contents do not outlive a
+ * call. */
+SK_API size_t sk_paged_pages_workspace_bytes(const sk_paged_layer* layer);
+
+/* Before an append of n_new[b] tokens to each request (device int32 [batch]; NULL: one
+ * each; <= 0: none), give every request the blocks it needs.  In this order:
+ *   1. with window > 0, blocks that hold no key the request's next query sees (the last
+ *      one's, if it has no new tokens) are given back: the entry becomes -1;
+ *   2. a request needs a block for each table entry of its new tokens that is empty
+ *      (outside [0, n_blocks)) or names a block with ref > 1.  Where such a shared block
+ *      already holds tokens (only the entry of token seq_lens[b] can) its contents are
+ *      copied in every pool of every layer; if all that hold it are about to write it, the
+ *      last of them keeps it.  Blocks held alone stay;
+ *   3. requests are served in order while the blocks that step 1 left free (ref 0) last;
+ *      from the first that does not get all of its blocks on, none is
+ *      (SK_DEVERR_CAPACITY).  New blocks are the lowest free ids in order.
+ * A request whose tokens would pass max_blocks (SK_DEVERR_CAPACITY), whose partly filled
+ * block is missing (SK_DEVERR_BLOCK_TABLE), whose length is negative (SK_DEVERR_STATE) or
+ * that needs more than 2^20 blocks (SK_DEVERR_CAPACITY) is refused alone.
+ *   granted: device int32 [batch]: 1 where the request may append, else 0 (its blocks are
+ *     as step 1 left them, and an append to it would write shared or missing blocks).
+ * seq_lens is read from layers[0] and not changed. */
+SK_API sk_status sk_paged_reserve(const sk_paged_layer* layers, int32_t n_layers, int32_t* ref,
+                                  const int32_t* n_new, int32_t* granted, void* workspace, size_t ws_bytes,
+                                  void* stream);
+
+/* Request b continues from request parents[b] as it was before the call (device int32
+ * [batch]): its table row, its length in every layer, a use more of each block; what row b
+ * held is given up.  parents[b] = b leaves it; -1 empties it (entries -1, length 0), which
+ * frees the blocks that no other request holds.  So one call reorders the beams of a
+ * search, forks a prompt into several requests, or releases finished ones; no page is
+ * copied until a shared one is written (sk_paged_reserve).  A parent outside [-1, batch)
+ * leaves its row as it was and sets SK_DEVERR_STATE. */
+SK_API sk_status sk_paged_fork(const sk_paged_layer* layers, int32_t n_layers, int32_t* ref,
+                               const int32_t* parents, void* stream);
+
+/* Move the blocks in use (ref > 0) to the lowest ids, in every pool of every layer: static
+ * sink blocks stay where they are, and of the n other blocks those behind the first n ids
+ * that are not static sink blocks move, in order, to the free ones among these.  Table
+ * entries and ref follow (an entry that named a free block becomes -1).
+ *   block_map: device int32 [n_blocks]: the new id of each block that was in use, -1 for
+ *     the others, for holds that the caller keeps elsewhere.
+ *   used: device int32 [1]: one past the highest id in use afterwards; the pool may be cut
+ *     there. */
+SK_API sk_status sk_paged_compact(const sk_paged_layer* layers, int32_t n_layers, int32_t* ref,
+                                  int32_t* block_map, int32_t* used, void* workspace, size_t ws_bytes,
+                                  void* stream);
 
 /* ---- 4-bit cache rows as values ----------------------------------------------------- */
 

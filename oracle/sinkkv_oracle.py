@@ -624,6 +624,112 @@ def paged_decode_attention(q_rot: np.ndarray, k_pool: np.ndarray, v_pool: np.nda
 
 
 # ---------------------------------------------------------------------------
+# Page operations, one request after the other (the library's rules; the source pages leave
+# allocation to the engine).
+# ---------------------------------------------------------------------------
+
+def pages_reserve(table: np.ndarray, ref: np.ndarray, lens: Sequence[int], n_new: Sequence[int], block_size: int,
+                  sinks: int, window: int, sink_len: int):
+    """Changes table [B, MB] and ref [NB] in place; returns (granted, copies) with copies a list
+    of (block, its copy)."""
+    B, MB = table.shape
+    NB = len(ref)
+
+    def valid(e):
+        return 0 <= e < NB
+
+    if window > 0:
+        for b in range(B):
+            keep = lens[b] + sink_len + max(0, min(1, n_new[b])) - window      # logical keys from here on are seen
+            for j in range(MB):
+                lo = sink_len + j * block_size
+                if valid(table[b, j]) and lo + block_size <= keep and lo >= sinks:
+                    ref[table[b, j]] -= 1
+                    table[b, j] = -1
+    before = ref.copy()
+    wants, status = [], []
+    for b in range(B):
+        L, n = lens[b], n_new[b]
+        w = []
+        if n <= 0:
+            status.append("nothing")
+        elif L < 0 or L + n > MB * block_size:
+            status.append("refused")
+        elif L % block_size and not valid(table[b, L // block_size]):
+            status.append("refused")
+        else:
+            status.append("asks")
+            for j in range(L // block_size, (L + n - 1) // block_size + 1):
+                e = table[b, j]
+                if not valid(e) or before[e] > 1:
+                    w.append(j)
+        wants.append(w)
+    # shared blocks in which a request's next token falls
+    shared = {}
+    for b in range(B):
+        if status[b] == "asks" and lens[b] % block_size:
+            e = table[b, lens[b] // block_size]
+            if before[e] > 1:
+                shared.setdefault(int(e), []).append(b)
+    for e, who in shared.items():
+        if len(who) == before[e]:
+            wants[who[-1]].remove(lens[who[-1]] // block_size)
+    free = [i for i in range(NB) if before[i] == 0]
+    granted, copies, out = [], [], False
+    for b in range(B):
+        if status[b] != "asks":
+            granted.append(1 if status[b] == "nothing" else 0)
+            continue
+        if out or len(wants[b]) > len(free):
+            out = True
+            granted.append(0)
+            continue
+        granted.append(1)
+        for j in wants[b]:
+            e, new = int(table[b, j]), free.pop(0)
+            if valid(e):
+                ref[e] -= 1
+                if j == lens[b] // block_size and lens[b] % block_size:
+                    copies.append((e, new))
+            ref[new] = 1
+            table[b, j] = new
+    return granted, copies
+
+
+def pages_fork(table: np.ndarray, ref: np.ndarray, lens: np.ndarray, parents: Sequence[int]):
+    """Changes table, ref and lens [layers, B] in place."""
+    was, was_lens = table.copy(), lens.copy()
+    for b, parent in enumerate(parents):
+        if parent == b or not -1 <= parent < len(was):
+            continue
+        for e in was[b]:
+            if 0 <= e < len(ref):
+                ref[e] -= 1
+        table[b] = -1 if parent < 0 else was[parent]
+        lens[:, b] = 0 if parent < 0 else was_lens[:, parent]
+        for e in table[b]:
+            if 0 <= e < len(ref):
+                ref[e] += 1
+
+
+def pages_compact(table: np.ndarray, ref: np.ndarray, fixed: Sequence[int]):
+    """Changes table and ref in place; returns (block_map, used, moves)."""
+    NB = len(ref)
+    fixed = set(int(x) for x in fixed)
+    movable = [i for i in range(NB) if ref[i] > 0 and i not in fixed]
+    places = [i for i in range(NB) if i not in fixed][:len(movable)]
+    holes = [i for i in places if ref[i] == 0]
+    moves = list(zip([i for i in movable if i not in set(places)], holes))
+    block_map = np.array([i if ref[i] > 0 else -1 for i in range(NB)])
+    for src, dst in moves:
+        block_map[src] = dst
+        ref[dst], ref[src] = ref[src], 0
+    inside = (table >= 0) & (table < NB)
+    table[inside] = block_map[table[inside]]
+    return block_map, int(block_map.max()) + 1, moves
+
+
+# ---------------------------------------------------------------------------
 # 4-bit cache rows (the library's own format; no page gives one).
 # ---------------------------------------------------------------------------
 

@@ -18,6 +18,8 @@ sk_kv_rerotate         kv_rerotate
 sk_kv_shift_recent     kv_shift_recent
 sk_paged_*             PagedLayer, paged_append, paged_decode_attention
 sk_kv4_unpack          kv4_unpack (+ kv4_row_bytes)
+sk_paged_reserve, sk_paged_fork, sk_paged_compact
+                       PagedGroup
 """
 from __future__ import annotations
 
@@ -130,6 +132,15 @@ _SIGNATURES = [
                                                  ctypes.c_size_t, ctypes.c_void_p]),
     ("sk_kv_shift_recent", ctypes.c_int, [ctypes.POINTER(KVLayerStruct), ctypes.c_int32, ctypes.c_void_p,
                                           ctypes.c_int32, ctypes.c_void_p]),
+    ("sk_paged_pages_workspace_bytes", ctypes.c_size_t, [ctypes.POINTER(PagedLayerStruct)]),
+    ("sk_paged_reserve", ctypes.c_int, [ctypes.POINTER(PagedLayerStruct), ctypes.c_int32, ctypes.c_void_p,
+                                        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
+                                        ctypes.c_void_p]),
+    ("sk_paged_fork", ctypes.c_int, [ctypes.POINTER(PagedLayerStruct), ctypes.c_int32, ctypes.c_void_p,
+                                     ctypes.c_void_p, ctypes.c_void_p]),
+    ("sk_paged_compact", ctypes.c_int, [ctypes.POINTER(PagedLayerStruct), ctypes.c_int32, ctypes.c_void_p,
+                                        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
+                                        ctypes.c_void_p]),
     ("sk_kv4_unpack", ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p,
                                      ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p]),
     ("sk_sync_check", ctypes.c_int, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
@@ -658,6 +669,79 @@ def paged_decode_attention(layer: PagedLayer, q_rot: torch.Tensor, out: Optional
                                             workspace.numel() * workspace.element_size(), _stream(stream)),
            "sk_paged_decode_attention")
     return out
+
+
+class PagedGroup:
+    """The blocks of paged layers that share one block table (sk_paged_reserve / fork /
+    compact).  ``ref``: int32 [n_blocks] uses of each block (default: an empty pool, with
+    one use for each static sink block, whose ids are then read from the device).  The
+    group works on the tensors that the layers hold when it is made; replacing one of them
+    takes a new group.  It owns one workspace: calls of one group on several streams must
+    be ordered (they change the same table anyway)."""
+
+    def __init__(self, layers: Sequence[PagedLayer], ref: Optional[torch.Tensor] = None):
+        if len(layers) == 0:
+            raise ValueError("a group needs a layer")
+        self.layers = list(layers)
+        L = self.layers[0]
+        dev, n_blocks = L.k_pool.device, L.k_pool.shape[0]
+        if ref is None:
+            ref = torch.zeros(n_blocks, dtype=torch.int32, device=dev)
+            if L.sink_block_ids is not None:
+                ref[L.sink_block_ids.long()] = 1
+        _check_i32("ref", ref, n_blocks, dev)
+        self.ref = ref
+        for x in self.layers:
+            _need_contig(x.k_pool, x.v_pool, x.block_table, x.seq_lens)
+        self._structs = (PagedLayerStruct * len(self.layers))(*[x.struct() for x in self.layers])
+        self._tensors = [(x.k_pool, x.v_pool, x.block_table, x.sink_block_ids, x.seq_lens, x.err) for x in self.layers]
+        need = int(_lib().sk_paged_pages_workspace_bytes(self._structs))
+        if need == 0:
+            raise SinkKVError(SK_ERR_UNSUPPORTED, "sk_paged_pages_workspace_bytes")
+        self._ws = torch.empty(need, dtype=torch.uint8, device=dev)
+
+    @property
+    def batch(self):
+        return self.layers[0].batch
+
+    def reserve(self, n_new: Optional[torch.Tensor] = None, granted: Optional[torch.Tensor] = None,
+                stream=None) -> torch.Tensor:
+        """Blocks for n_new[b] new tokens of each request (int32 [batch]; None: one each).
+        Returns granted, int32 [batch]: 1 where the request may append."""
+        dev = self.ref.device
+        if n_new is not None:
+            _check_i32("n_new", n_new, self.batch, dev)
+        if granted is None:
+            granted = torch.empty(self.batch, dtype=torch.int32, device=dev)
+        else:
+            _check_i32("granted", granted, self.batch, dev)
+        _check(_lib().sk_paged_reserve(self._structs, len(self.layers), _ptr(self.ref), _ptr(n_new), _ptr(granted),
+                                       _ptr(self._ws), self._ws.numel(), _stream(stream)), "sk_paged_reserve")
+        return granted
+
+    def fork(self, parents: torch.Tensor, stream=None):
+        """Request b continues from request parents[b] (int32 [batch]; b: stays, -1: released)."""
+        _check_i32("parents", parents, self.batch, self.ref.device)
+        _check(_lib().sk_paged_fork(self._structs, len(self.layers), _ptr(self.ref), _ptr(parents), _stream(stream)),
+               "sk_paged_fork")
+
+    def compact(self, block_map: Optional[torch.Tensor] = None, stream=None):
+        """Blocks in use to the lowest ids.  Returns (block_map int32 [n_blocks]: new ids, -1
+        for blocks that were free; used int32 [1]: one past the highest id in use)."""
+        dev = self.ref.device
+        if block_map is None:
+            block_map = torch.empty_like(self.ref)
+        else:
+            _check_i32("block_map", block_map, self.ref.numel(), dev)
+        used = torch.empty(1, dtype=torch.int32, device=dev)
+        _check(_lib().sk_paged_compact(self._structs, len(self.layers), _ptr(self.ref), _ptr(block_map), _ptr(used),
+                                       _ptr(self._ws), self._ws.numel(), _stream(stream)), "sk_paged_compact")
+        return block_map, used
+
+
+def _check_i32(name: str, t: torch.Tensor, n: int, device):
+    if t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be a contiguous int32 tensor of {n} values on {device}")
 
 
 def kv4_unpack(rows: torch.Tensor, dtype=torch.bfloat16, stream=None):
