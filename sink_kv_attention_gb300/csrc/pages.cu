@@ -103,6 +103,8 @@ constexpr int kMostBlocks = 1 << 20;  // for one request in one call: the scans 
 constexpr int kRefused = -1;  // the request cannot be served whatever the pool holds
 constexpr int kNothing = -2;  // nothing asked for
 
+constexpr int kAhead = 8;     // table entries a lane looks at together (their loads overlap)
+
 // The request's part of a block table row that its new tokens fall into.
 struct Wanted {
     int64_t len;
@@ -119,6 +121,22 @@ struct Wanted {
         partial = fits && n > 0 && (len & ((int64_t(1) << p.bs_log2) - 1)) != 0;
     }
 };
+
+// Table entries j, j + 32, .. up to `last`: the block, or -1 for one outside the pool (or past
+// `last`), and whether it is shared.
+__device__ __forceinline__ void load_entries(const ReserveParams& p, const int32_t* row, int64_t j, int last,
+                                             int32_t* e, bool* shared) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) e[u] = j + 32 * u <= last ? row[j + 32 * u] : -1;
+    int32_t r[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+        if (e[u] < 0 || e[u] >= p.NB) e[u] = -1;
+        r[u] = e[u] >= 0 ? __ldcg(p.ref + e[u]) : 0;
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) shared[u] = r[u] > 1;
+}
 
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1) reserve_kernel(ReserveParams p) {
     __shared__ int s_scan[kAllWarps + kWarps];
@@ -142,12 +160,16 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1) 
             const int64_t j0 = (max(0, p.S - p.sink_len) + bs - 1) >> p.bs_log2;
             const int64_t j1 = keep > 0 ? min(keep >> p.bs_log2, int64_t(p.MB)) : 0;
             int32_t* row = p.table + int64_t(b) * p.MB;
-            for (int64_t j = j0 + lane; j < j1; j += 32) {
-                const int32_t e = row[j];
-                if (e >= 0 && e < p.NB) {
-                    row[j] = -1;
-                    atomicSub(p.ref + e, 1);
-                }
+            for (int64_t j = j0 + lane; j < j1; j += 32 * kAhead) {
+                int32_t e[kAhead];
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) e[u] = j + 32 * u < j1 ? row[j + 32 * u] : -1;
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u)
+                    if (e[u] >= 0 && e[u] < p.NB) {
+                        row[j + 32 * u] = -1;
+                        atomicSub(p.ref + e[u], 1);
+                    }
             }
         }
         cluster_sync();
@@ -162,20 +184,21 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1) 
             need = kNothing;
         } else if (ok) {
             const int32_t* row = p.table + int64_t(b) * p.MB;
-            for (int j0 = w.first; j0 <= w.last; j0 += 32) {
-                const int j = j0 + lane;
-                bool alloc = false, bad = false;
-                if (j <= w.last) {
-                    const int32_t e = row[j];
-                    const bool valid = e >= 0 && e < p.NB;
-                    const bool sh = valid && __ldcg(p.ref + e) > 1;
-                    alloc = !valid || sh;
-                    bad = j == w.first && w.partial && !valid;
-                    if (j == w.first && w.partial && sh) shared = e;
+            for (int64_t j0 = w.first; j0 <= w.last; j0 += 32 * kAhead) {
+                int32_t e[kAhead];
+                bool sh[kAhead];
+                load_entries(p, row, j0 + lane, w.last, e, sh);
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    const int64_t j = j0 + lane + 32 * u;
+                    need += __popc(__ballot_sync(kFull, j <= w.last && (e[u] < 0 || sh[u])));
+                    if (j == w.first && w.partial) {
+                        if (e[u] < 0) ok = false;
+                        else if (sh[u]) shared = e[u];
+                    }
                 }
-                need += __popc(__ballot_sync(kFull, alloc));
-                ok = ok && !__any_sync(kFull, bad);
             }
+            ok = __all_sync(kFull, ok);
             shared = __shfl_sync(kFull, shared, 0);  // entry `first` was lane 0's
             if (!ok && lane == 0) set_error(p.err, SK_DEVERR_BLOCK_TABLE);
             if (need > kMostBlocks) {
@@ -252,29 +275,28 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1) 
             const Wanted w(p, b2);
             int32_t* row = p.table + int64_t(b2) * p.MB;
             const bool keep = s_keeps[b2];
-            for (int j0 = w.first; j0 <= w.last; j0 += 32) {
-                const int j = j0 + lane;
-                bool alloc = false, shared_block = false;
-                int32_t e = -1;
-                if (j <= w.last) {
-                    e = row[j];
-                    const bool valid = e >= 0 && e < p.NB;
-                    shared_block = valid && __ldcg(p.ref + e) > 1;  // counts of shared blocks change below
-                    alloc = (!valid || shared_block) && !(keep && j == w.first);
-                }
-                const uint32_t m = __ballot_sync(kFull, alloc);
-                if (alloc) {
-                    const int r = base + __popc(m & ((1u << lane) - 1));
-                    const int32_t id = __ldcg(p.free_ids + r);
-                    row[j] = id;
-                    p.ref[id] = 1;
-                    p.old_ids[r] = shared_block ? e : -1;
-                    if (shared_block && j == w.first && w.partial) {
-                        src = e;
-                        dst = id;
+            for (int64_t j0 = w.first; j0 <= w.last; j0 += 32 * kAhead) {
+                int32_t e[kAhead];
+                bool sh[kAhead];  // the counts of shared blocks change below
+                load_entries(p, row, j0 + lane, w.last, e, sh);
+#pragma unroll
+                for (int u = 0; u < kAhead; ++u) {
+                    const int64_t j = j0 + lane + 32 * u;
+                    const bool alloc = j <= w.last && (e[u] < 0 || sh[u]) && !(keep && j == w.first);
+                    const uint32_t m = __ballot_sync(kFull, alloc);
+                    if (alloc) {
+                        const int r = base + __popc(m & ((1u << lane) - 1));
+                        const int32_t id = __ldcg(p.free_ids + r);
+                        row[j] = id;
+                        p.ref[id] = 1;
+                        p.old_ids[r] = sh[u] ? e[u] : -1;
+                        if (sh[u] && j == w.first && w.partial) {
+                            src = e[u];
+                            dst = id;
+                        }
                     }
+                    base += __popc(m);
                 }
-                base += __popc(m);
             }
         }
         src = __shfl_sync(kFull, src, 0);
