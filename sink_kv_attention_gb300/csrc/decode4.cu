@@ -90,7 +90,7 @@ template <typename T, int D, int NREP, int KVH> struct Cfg4 {
     static constexpr size_t OFF_Q = size_t(NWARPS) * SLOTS * SLOT_BYTES;
     static constexpr size_t OFF_BAR = OFF_Q + 2 * Q_BYTES;       // slot barriers, then two of the q rows
     static constexpr size_t OFF_ROWS = OFF_BAR + (NWARPS * SLOTS + 2) * 8;   // Rows4
-    static constexpr size_t OFF_M = (OFF_ROWS + (2 * kMaxBatch + 2) * 8 + 15) / 16 * 16;  // the warps' (m, l) per head
+    static constexpr size_t OFF_M = (OFF_ROWS + (3 * kMaxBatch + 1) * 8 + 15) / 16 * 16;  // the warps' (m, l) per head
     static constexpr size_t OFF_FLAGS = OFF_M + 2 * HEADS * NWARPS * 4;      // slot of each warp's sums
     static constexpr size_t SMEM = OFF_FLAGS + NWARPS * 4 + 2 * sizeof(Cut4);
     static constexpr int THREADS = NWARPS * 32;
@@ -165,6 +165,7 @@ __device__ __forceinline__ int64_t div_rows(int64_t a, int64_t b) {  // a, b >= 
 struct Rows4 {
     int64_t* start;  // [B + 1]
     int64_t* len;    // [B]
+    int64_t* shift;  // [B] paged: rows behind the sinks hold key row + shift (0: every row its key)
 };
 
 // The units of a share, in order.  A share has fewer than 2^31 rows (its rows are bytes of
@@ -203,56 +204,59 @@ struct Units4 {
 };
 
 // The tiles of a block's share that fall to one warp, in order: tile i of the share
-// (counted over all its units) goes to warp i % NWARPS.
-template <int NWARPS, int TR>
+// (counted over all its units) goes to warp i % NWARPS.  Tiles of a paged unit end where the
+// key is a multiple of TR, so that they lie in as few pages as possible; the first may be
+// shorter.
+template <int NWARPS, int TR, bool PAGED>
 struct TileWalk {
     Units4 u;
     int warp0;             // the warp that takes the unit's first tile
-    int at, left;          // this warp's tile: first row - r0, rows from there to the part's end
-    __device__ __forceinline__ void unit(int warp) {
-        at = (warp >= warp0 ? warp - warp0 : warp + NWARPS - warp0) * TR;
+    int at, left;          // this warp's tile: its first row - r0 (negative for a short first tile: the
+                           // tile starts at 0), and the part's end - at
+    __device__ __forceinline__ int lead(const Rows4& rows) const {  // rows that the first tile lacks
+        return PAGED ? int(u.r0 + rows.shift[u.b]) & (TR - 1) : 0;
+    }
+    __device__ __forceinline__ void unit(const Rows4& rows, int warp) {
+        at = (warp >= warp0 ? warp - warp0 : warp + NWARPS - warp0) * TR - lead(rows);
         left = u.rows - at;
     }
     __device__ __forceinline__ void begin(const Rows4& rows, int B, int64_t lo, int64_t hi, int warp) {
         u.begin(rows, B, lo, hi);
         warp0 = 0;
-        unit(warp);
+        unit(rows, warp);
     }
     __device__ __forceinline__ void step() {
         at += NWARPS * TR;
         left -= NWARPS * TR;
     }
     __device__ __forceinline__ bool next_unit(const Rows4& rows, int Hu, int warp) {
-        const int tiles = (u.rows + TR - 1) / TR;
+        const int tiles = (u.rows + lead(rows) + TR - 1) / TR;
         if (!u.next(rows, Hu)) return false;
         warp0 = (warp0 + tiles) % NWARPS;
-        unit(warp);
+        unit(rows, warp);
         return true;
     }
+    __device__ __forceinline__ int first() const { return PAGED ? max(at, 0) : at; }
+    __device__ __forceinline__ int count() const { return PAGED ? min(left, TR) + min(at, 0) : min(left, TR); }
 };
 
 // The loading side of a warp's walk: the current tile's source.
 template <typename C, int KVH, bool PAGED>
 struct Loader {
-    TileWalk<C::NWARPS, C::TR> t;
+    TileWalk<C::NWARPS, C::TR, PAGED> t;
     const uint8_t* src;   // contiguous: the tile's rows of the unit's first kv head
-    int64_t key0;         // paged: key of row r0 (at rows below `sinks_end`: the row itself)
-    int sinks_end;        // paged: offset from r0 at which the window's rows begin (at or before 0: all are)
+    // paged, of row lane % TR of the tile: its key, and the pool block that the table names,
+    // looked up when the tile before is loaded (its latency is then hidden)
+    int64_t key;
+    int32_t block;
     bool more;
     __device__ __forceinline__ void source(const DecodeParams& p) {
-        if constexpr (!PAGED) {
+        if constexpr (!PAGED)
             src = static_cast<const uint8_t*>(p.kc) +
                   ((int64_t(t.u.b) * p.Hkv + t.u.g) * KVH * p.cap + t.u.r0 + t.at) * C::ROWB;
-        } else {
-            const int64_t n_req = p.pos[t.u.b];
-            const int64_t Lk = n_req > 0 ? n_req + p.sink_len : 0;
-            const bool split = p.W > 0 && Lk > int64_t(p.S) + p.W;  // sinks, then the last W keys
-            key0 = split ? Lk - p.W - p.S + t.u.r0 : t.u.r0;            // of a window row
-            sinks_end = split ? int(max(int64_t(-1), min(int64_t(p.S) - t.u.r0, int64_t(0x7fffffff)))) : -1;
-        }
     }
     // moves on to a unit with a tile for this warp
-    __device__ __forceinline__ void settle(const DecodeParams& p, const Rows4& rows, int warp) {
+    __device__ __forceinline__ void settle(const DecodeParams& p, const Rows4& rows, int warp, int lane) {
         bool moved = false;
         while (t.left <= 0) {
             if (!t.next_unit(rows, p.Hkv, warp)) {
@@ -262,24 +266,38 @@ struct Loader {
             moved = true;
         }
         if (moved) source(p);
+        if constexpr (PAGED) {
+            const int i = lane % C::TR;
+            const int64_t row = t.u.r0 + t.first() + i;
+            key = row < p.S ? row : row + rows.shift[t.u.b];
+            block = -1;
+            if (i < t.count()) {
+                if (key < p.sink_len) {
+                    block = p.sink_blocks[key >> p.bs_log2];
+                } else {
+                    const int64_t j = (key - p.sink_len) >> p.bs_log2;
+                    if (j < p.max_blocks) block = p.block_table[int64_t(t.u.b) * p.max_blocks + j];
+                }
+            }
+        }
     }
-    __device__ __forceinline__ void begin(const DecodeParams& p, const Rows4& rows, int warp) {
+    __device__ __forceinline__ void begin(const DecodeParams& p, const Rows4& rows, int warp, int lane) {
         more = true;
         source(p);
-        settle(p, rows, warp);
+        settle(p, rows, warp, lane);
     }
-    __device__ __forceinline__ void step(const DecodeParams& p, const Rows4& rows, int warp) {
+    __device__ __forceinline__ void step(const DecodeParams& p, const Rows4& rows, int warp, int lane) {
         t.step();
         if constexpr (!PAGED) src += C::NWARPS * C::HEAD_BYTES;
-        settle(p, rows, warp);
+        settle(p, rows, warp, lane);
     }
     // Fills `slot` with the tile (the whole warp): the rows of each kv head of the unit, one
-    // after the other.  Contiguous: one copy per kv head.  Paged: lane kv TR + i finds the
-    // pool row of the tile's row i; the first row of each run of consecutive pool rows
-    // copies the run.
+    // after the other.  Contiguous: one copy per kv head.  Paged: lane kv TR + i has row i of
+    // kv head kv; the first row of each run of consecutive pool rows copies the run (both kv
+    // heads at once where the tile is a whole page).
     __device__ __forceinline__ void load(const DecodeParams& p, uint8_t* slot, uint64_t* bar, uint64_t policy,
                                          int lane, bool* bad) const {
-        const int n = min(t.left, C::TR);
+        const int n = t.count();
         if constexpr (!PAGED) {
             if (lane == 0) {
                 mbar_arrive_expect_tx(bar, uint32_t(KVH * n) * C::ROWB);
@@ -289,31 +307,25 @@ struct Loader {
                                   policy);
             }
         } else {
-            const int i = lane % C::TR, kv = lane / C::TR, off = t.at + i;
-            const int64_t key = off < sinks_end ? t.u.r0 + off : key0 + off;
+            const int i = lane % C::TR, kv = lane / C::TR;
             const bool active = i < n;
-            int64_t blk = 0;
-            if (active) {
-                if (key < p.sink_len) {
-                    blk = p.sink_blocks[key >> p.bs_log2];
-                } else {
-                    const int64_t j = (key - p.sink_len) >> p.bs_log2;
-                    blk = j < p.max_blocks ? p.block_table[int64_t(t.u.b) * p.max_blocks + j] : -1;
-                }
-                if (blk < 0 || blk >= p.pool_blocks) {
-                    *bad = true;
-                    blk = 0;  // stay inside the pool; the error word reports it
-                }
+            int64_t blk = block;
+            if (active && (blk < 0 || blk >= p.pool_blocks)) {
+                *bad = true;
+                blk = 0;  // stay inside the pool; the error word reports it
             }
             const int in = int(key) & (p.bs - 1);
-            const bool first = active && (i == 0 || in == 0 || off == sinks_end);
+            const bool jump = t.u.r0 + t.first() + i == p.S;  // the window's first row
+            const bool whole = KVH > 1 && p.bs == C::TR && n == C::TR &&
+                               __all_sync(kFull, in == i && !(jump && i > 0));
+            const bool first = active && (i == 0 || in == 0 || jump);
             const uint32_t firsts = __ballot_sync(kFull, first);
             if (lane == 0) mbar_arrive_expect_tx(bar, uint32_t(KVH * n) * C::ROWB);
             __syncwarp();
-            if (first) {
+            if (first && !(whole && kv > 0)) {
                 // rows up to the next run of this kv head, or to the tile's end
                 const uint32_t later = (lane == 31 ? 0u : firsts >> (lane + 1)) & ((1u << (C::TR - 1 - i)) - 1u);
-                const int len = later != 0 ? __ffs(int(later)) : n - i;
+                const int len = whole ? KVH * C::TR : (later != 0 ? __ffs(int(later)) : n - i);
                 const int64_t head = blk * (p.Hkv * KVH) + t.u.g * KVH + kv;
                 bulk_copy_g2s(slot + kv * C::HEAD_BYTES + i * C::ROWB,
                               static_cast<const uint8_t*>(p.kc) + (head * p.bs + in) * C::ROWB,
@@ -362,12 +374,24 @@ __device__ __forceinline__ void finish(const DecodeParams& p, int64_t unit, int 
 template <typename T, int D, int HEADS, int PF, int THREADS>
 __device__ __noinline__ void combine_unit(const DecodeParams& p, int64_t unit, const float* first, int n,
                                              float* w) {
+    constexpr int U = 16;  // partials in flight; the first are asked for before the weights are known
+    constexpr int VALS = HEADS * D / 4;
+    static_assert(VALS <= THREADS, "a thread per 4 values");
+    const int idx = min(int(threadIdx.x), VALS - 1), h = idx / (D / 4);
+    const float* part = first + idx * 4;
+    float4 v[U];
+    auto fetch = [&](int i0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (i0 + u < n) v[u] = __ldcg(reinterpret_cast<const float4*>(part + int64_t(i0 + u) * PF));
+    };
+    fetch(0);
     float* ls = w + n * HEADS;        // [n][HEADS] sums of weights
     float* top = ls + n * HEADS;      // [HEADS] reference, then the sum of weights
     for (int i = threadIdx.x; i < n * HEADS; i += THREADS) {
-        const float* part = first + int64_t(i / HEADS) * PF + HEADS * D + i % HEADS;
-        w[i] = __ldcg(part);
-        ls[i] = __ldcg(part + HEADS);
+        const float* ml = first + int64_t(i / HEADS) * PF + HEADS * D + i % HEADS;
+        w[i] = __ldcg(ml);
+        ls[i] = __ldcg(ml + HEADS);
     }
     __syncthreads();
     if (threadIdx.x < HEADS) {
@@ -382,29 +406,23 @@ __device__ __noinline__ void combine_unit(const DecodeParams& p, int64_t unit, c
         top[HEADS + threadIdx.x] = l;
     }
     __syncthreads();
-    for (int idx = threadIdx.x; idx < HEADS * D / 4; idx += THREADS) {
-        const int h = idx / (D / 4);
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-        const float* part = first + idx * 4;
-        constexpr int U = 8;  // partials in flight
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-        for (int i0 = 0; i0 < n; i0 += U) {
-            float4 v[U];
+    for (int i0 = 0;;) {
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (i0 + u < n) v[u] = __ldcg(reinterpret_cast<const float4*>(part + int64_t(i0 + u) * PF));
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (i0 + u >= n) break;
-                const float f = w[(i0 + u) * HEADS + h];
-                a.x = fmaf(v[u].x, f, a.x);
-                a.y = fmaf(v[u].y, f, a.y);
-                a.z = fmaf(v[u].z, f, a.z);
-                a.w = fmaf(v[u].w, f, a.w);
-            }
+        for (int u = 0; u < U; ++u) {
+            if (i0 + u >= n) break;
+            const float f = w[(i0 + u) * HEADS + h];
+            a.x = fmaf(v[u].x, f, a.x);
+            a.y = fmaf(v[u].y, f, a.y);
+            a.z = fmaf(v[u].z, f, a.z);
+            a.w = fmaf(v[u].w, f, a.w);
         }
-        finish<T, D, HEADS>(p, unit, h, idx % (D / 4) * 4, top[h], top[HEADS + h], a);
+        i0 += U;
+        if (i0 >= n) break;
+        fetch(i0);
     }
+    if (threadIdx.x < VALS) finish<T, D, HEADS>(p, unit, h, idx % (D / 4) * 4, top[h], top[HEADS + h], a);
     __syncthreads();
 }
 
@@ -437,7 +455,8 @@ __global__ void __launch_bounds__(Cfg4<T, D, NREP, KVH>::THREADS, 1) decode4_ker
     uint64_t* q_bars = all_bars + NWARPS * SLOTS;
     uint8_t* ring = smem + size_t(warp) * SLOTS * C::SLOT_BYTES;
     const Rows4 rows{reinterpret_cast<int64_t*>(smem + C::OFF_ROWS),
-                     reinterpret_cast<int64_t*>(smem + C::OFF_ROWS) + kMaxBatch + 1};
+                     reinterpret_cast<int64_t*>(smem + C::OFF_ROWS) + kMaxBatch + 1,
+                     reinterpret_cast<int64_t*>(smem + C::OFF_ROWS) + 2 * kMaxBatch + 1};
     float* warp_m = reinterpret_cast<float*>(smem + C::OFF_M);  // [HEADS][NWARPS] references
     float* warp_l = warp_m + HEADS * NWARPS;                    // [HEADS][NWARPS] sums, at the block's reference
     int* warp_slot = reinterpret_cast<int*>(smem + C::OFF_FLAGS);  // [NWARPS] where a warp's sums are; -1: none
@@ -460,7 +479,7 @@ __global__ void __launch_bounds__(Cfg4<T, D, NREP, KVH>::THREADS, 1) decode4_ker
     bool timed_out = false, bad = false;
     int64_t R = 0;
     int P = 0;
-    TileWalk<NWARPS, TR> w;
+    TileWalk<NWARPS, TR, PAGED> w;
 #pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {
         if (pass == 1) pdl_wait();  // the append has written the state, q and the new rows
@@ -468,8 +487,14 @@ __global__ void __launch_bounds__(Cfg4<T, D, NREP, KVH>::THREADS, 1) decode4_ker
         for (int b = threadIdx.x; b < p.B; b += C::THREADS) {
             int64_t n = visible_rows(p, b);
             n = max(int64_t(0), PAGED ? n : min(n, p.cap));
-            if (pass == 0 || rows.len[b] != n) {
+            int64_t shift = 0;
+            if constexpr (PAGED) {
+                const int64_t L = p.pos[b] > 0 ? p.pos[b] + p.sink_len : 0;
+                if (p.W > 0 && L > int64_t(p.S) + p.W) shift = L - p.W - p.S;
+            }
+            if (pass == 0 || rows.len[b] != n || (PAGED && rows.shift[b] != shift)) {
                 rows.len[b] = n;
+                if (PAGED) rows.shift[b] = shift;
                 changed = true;
             }
         }
@@ -528,12 +553,12 @@ __global__ void __launch_bounds__(Cfg4<T, D, NREP, KVH>::THREADS, 1) decode4_ker
     int n_cuts = 0;
     Loader<C, KVH, PAGED> ld;
     ld.t = w;
-    ld.begin(p, rows, warp);
+    ld.begin(p, rows, warp, lane);
     int slot = 0;
     uint32_t phase = 0;
     for (int s = 0; s < SLOTS && ld.more; ++s) {
         ld.load(p, ring + s * C::SLOT_BYTES, &bars[s], policy, lane, &bad);
-        ld.step(p, rows, warp);
+        ld.step(p, rows, warp, lane);
     }
 
     const uint32_t half_sel = (g8 & 1) ? 0x7632u : 0x5410u;  // which 4 codes of a word of 8 are this lane's
@@ -627,7 +652,7 @@ __global__ void __launch_bounds__(Cfg4<T, D, NREP, KVH>::THREADS, 1) decode4_ker
 
         int last = -1;  // the slot of the warp's last tile of the unit
         for (; w.left > 0; w.step()) {
-            const int n = w.left;  // rows of the tile, if fewer than TR
+            const int n = w.count();
             uint8_t* tile = ring + slot * C::SLOT_BYTES;
             if (!mbar_wait_bounded(&bars[slot], phase)) timed_out = true;
             if (n < TR) {  // rows past the tile's last one: zeros (whatever the slot held)
@@ -801,9 +826,9 @@ __global__ void __launch_bounds__(Cfg4<T, D, NREP, KVH>::THREADS, 1) decode4_ker
             // of the warp's last tile of the unit is refilled after the merge, which uses it.
             if (n < TR) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
-            if (ld.more && n > NWARPS * TR) {
+            if (ld.more && w.left > NWARPS * TR) {
                 ld.load(p, tile, &bars[slot], policy, lane, &bad);
-                ld.step(p, rows, warp);
+                ld.step(p, rows, warp, lane);
             }
             last = slot;
             if (++slot == SLOTS) { slot = 0; phase ^= 1; }
@@ -906,7 +931,7 @@ __global__ void __launch_bounds__(Cfg4<T, D, NREP, KVH>::THREADS, 1) decode4_ker
         __syncthreads();
         if (last >= 0 && ld.more) {
             ld.load(p, ring + last * C::SLOT_BYTES, &bars[last], policy, lane, &bad);
-            ld.step(p, rows, warp);
+            ld.step(p, rows, warp, lane);
         }
         if (threadIdx.x == 0 && q_more) load_q(q_at);
         if (++q_at == 2) { q_at = 0; q_phase ^= 1; }
