@@ -17,15 +17,24 @@
 // the tensor cores take exactly: a word of 8 codes becomes 4 operand registers with 4
 // ANDs and a shift, and the factors 2^24 / 2^20 are undone on q (even / odd nibbles) and
 // on the finished output.  q is scaled by a power of two per head to sit at the top of
-// fp16's range (bf16 q: exact; fp32 q: in two fp16 parts, 22 bits).  The per-group scale
+// fp16's range (bf16 q: exact; fp32 q: in two fp16 parts, 24 bits).  The per-group scale
 // and minimum are applied in fp32 to the products of K; for V the scale goes into the
 // probabilities, and the minimum is summed in fp32.
+//
+// The tensor core adds a step's products and the accumulator after cutting each, towards 0,
+// to the precision of the largest as its exponents tell, which for subnormal operands is up
+// to 2^10 too large: sums are good to about 2^-18 of the largest product (measured: rms
+// 2^-22, 2^-26 with normal operands).  That is far below a bf16 output.  fp32 calls turn the
+// codes into normal fp16 integers around 0 (code - 8, and m + 8 s for m: an OR and a
+// subtraction more), make the upper parts of q and of P' multiples of one unit, so that their
+// products add exactly, and add lower parts, upper parts and a tile's sums to the running
+// ones in fp32 (six fp32 keys against 64 bits: 3e-6 before, 3e-7 so).
 //
 // P' = p s_grp is rounded to fp16 (11 bits; fp32 io: two parts).  Its range is kept by
 // the reference of the online softmax: weights are 2^(score - mref) with
 // mref = (running max of the head) + (exponent of the largest V scale seen) - kHead, so
-// that P' <= 2^(kHead + kSlack + 1) < 65504.  The running max is only moved when a score
-// passes it by kSlack (a factor 2^8 of room), which in practice is once per unit: the
+// that P' < 2^(kHead + kSlack + 1) < 65504.  The running max is only moved when a score
+// passes it by kSlack (bf16: a factor 2^8 of room), which in practice is once per unit: the
 // vote costs less than a reduction per tile.  Row sums are of the unrounded fp32 weights.
 //
 // Work split: the visible rows of all units (a sequence and one or two kv heads) are laid
@@ -62,8 +71,10 @@ namespace sk {
 namespace {
 
 constexpr float kRefNone = -1e30f;  // reference of a head that has seen no key
-constexpr int kHead = 6;            // log2 of the weight at the reference, V scale 1
-constexpr float kSlack = 8.0f;      // a score may pass the reference by this much
+// log2 of the weight at the reference, V scale 1, and how far a score may pass the reference.
+// fp32 calls leave no slack: their weights' upper parts are multiples of a fixed unit.
+template <bool F32> constexpr int kHead = F32 ? 13 : 6;
+template <bool F32> constexpr float kSlack = F32 ? 0.0f : 8.0f;
 constexpr int kExpFloor = -60;      // V scales below 2^-60 are taken as 2^-60 in the reference
 constexpr uint32_t kLowNibbles = 0x000F000Fu, kHighNibbles = 0x00F000F0u;
 
@@ -80,7 +91,8 @@ template <typename T, int D, int NREP, int KVH> struct Cfg4 {
     static constexpr int ROWB = kv4_row_bytes(D);
     static constexpr int HEADS = NREP * KVH;               // q heads of a unit
     static constexpr int TR = 32 / KVH;                    // rows of a tile (of each kv head)
-    static constexpr int NWARPS = HEADS == 8 && KVH == 1 ? 8 : 12;
+    // 12 warps where their registers allow (measured: 8 warps 4-10% slower on bf16 calls)
+    static constexpr int NWARPS = (HEADS == 8 && KVH == 1) || sizeof(T) == 4 ? 8 : 12;
     static constexpr int HEAD_BYTES = TR * ROWB;           // a kv head's rows in a slot
     static constexpr int SLOT_BYTES = KVH * HEAD_BYTES;
     static constexpr int SLOTS = NWARPS == 8 ? 4 : 3;
@@ -141,6 +153,27 @@ __device__ __forceinline__ float2 half2_floats(uint32_t w) {
 __device__ __forceinline__ uint32_t half2_times(uint32_t w, __half2 f) {
     const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&w), f);
     return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// A masked word as the M side takes it: as it stands (subnormals), or as fp16 integers
+// code - 8 (HIGH: 16 (code - 8)).
+template <bool F32, bool HIGH> __device__ __forceinline__ uint32_t codes_of(uint32_t masked) {
+    if constexpr (!F32) return masked;
+    const uint32_t w = masked | 0x64006400u;  // 1024 + code (or + 16 code)
+    const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&w), __float2half2_rn(HIGH ? 1152.0f : 1032.0f));
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// (s, m) of a parameter word, m the value of the code that counts as 0.
+template <bool F32> __device__ __forceinline__ float2 scale_and_zero(uint32_t par) {
+    const float s = __uint_as_float(par & 0xFFFF0000u), m = __uint_as_float(par << 16);
+    return make_float2(s, F32 ? fmaf(8.0f, s, m) : m);
+}
+
+// x to the nearest multiple of 2^e (|x| < 2^(e + 22)).
+template <int e> __device__ __forceinline__ float to_multiple(float x) {
+    constexpr float magic = 12582912.0f * float(1 << e);  // 1.5 * 2^23 units
+    return __fadd_rn(__fadd_rn(x, magic), -magic);
 }
 
 __device__ __forceinline__ float pow2f(int e) { return __uint_as_float(uint32_t(e + 127) << 23); }  // normal range
@@ -561,6 +594,8 @@ __global__ void __launch_bounds__(Cfg4<T, D, NREP, KVH>::THREADS, 1) decode4_ker
         ld.step(p, rows, warp, lane);
     }
 
+    auto low = [](uint32_t w) { return codes_of<F32, false>(w & kLowNibbles); };
+    auto high = [](uint32_t w) { return codes_of<F32, true>(w & kHighNibbles); };
     const uint32_t half_sel = (g8 & 1) ? 0x7632u : 0x5410u;  // which 4 codes of a word of 8 are this lane's
     const int my_kv = KVH == 1 ? 0 : t4 >> 1;                // kv head of the lane's columns
     // this lane's places in a slot: K words of row kappa(g8), parameters of that row (of the
@@ -601,7 +636,7 @@ __global__ void __launch_bounds__(Cfg4<T, D, NREP, KVH>::THREADS, 1) decode4_ker
             amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
             // 2^e puts the largest |q| into [2^14, 2^15)
             const int e = amax > 0.0f ? max(-102, min(14 - (int(__float_as_uint(amax) >> 23) - 127), 100)) : 0;
-            fac = p.qscale * pow2f(24 - e);
+            fac = p.qscale * pow2f((F32 ? 0 : 24) - e);
             const float f0 = pow2f(e), f1 = pow2f(e - 4);  // even / odd nibbles
 #pragma unroll
             for (int r = 0; r < NG; ++r)
@@ -610,7 +645,12 @@ __global__ void __launch_bounds__(Cfg4<T, D, NREP, KVH>::THREADS, 1) decode4_ker
                     float x = qf[r][i] * ((i & 1) ? f1 : f0), y = qf[r][i + 4] * ((i & 1) ? f1 : f0);
 #pragma unroll
                     for (int h = 0; h < NQ; ++h) {
-                        const uint32_t bits = half2_bits(x, y);
+                        // fp32, the upper part: a multiple of 2^4 (even; 2^0 odd) below 2^15 (2^11)
+                        const bool upper = F32 && h == 0;
+                        const uint32_t bits =
+                            !upper ? half2_bits(x, y)
+                                   : ((i & 1) ? half2_bits(to_multiple<0>(x), to_multiple<0>(y))
+                                              : half2_bits(to_multiple<4>(x), to_multiple<4>(y)));
                         const float2 part = half2_floats(bits);
                         x -= part.x;
                         y -= part.y;
@@ -624,15 +664,18 @@ __global__ void __launch_bounds__(Cfg4<T, D, NREP, KVH>::THREADS, 1) decode4_ker
         float2 qsum[NG];
 #pragma unroll
         for (int r = 0; r < NG; ++r) {
+            const uint32_t one = F32 ? 0x3C003C00u : 0x00010001u, sixteen = F32 ? 0x4C004C00u : 0x00100010u;
             float a[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int kv = 0; kv < KVH; ++kv)
 #pragma unroll
-                for (int h = 0; h < NQ; ++h)
-#pragma unroll
-                    for (int i = 0; i < 4; i += 2)
-                        mma16816(a, 0x00010001u, 0x00010001u, 0x00100010u, 0x00100010u, qb[kv][h][r][i],
-                                 qb[kv][h][r][i + 1]);
+                for (int h = NQ - 1; h >= 0; --h) {
+                    float part[4];
+                    mma16816_first(part, one, one, sixteen, sixteen, qb[kv][h][r][0], qb[kv][h][r][1]);
+                    mma16816(part, one, one, sixteen, sixteen, qb[kv][h][r][2], qb[kv][h][r][3]);
+                    a[0] += part[0];
+                    a[1] += part[1];
+                }
             qsum[r] = make_float2(a[0], a[1]);
         }
 
@@ -678,18 +721,19 @@ __global__ void __launch_bounds__(Cfg4<T, D, NREP, KVH>::THREADS, 1) decode4_ker
 #pragma unroll
                     for (int r = 0; r < NG; ++r) {
                         const uint32_t x = kw[0][r] >> 8, y = kw[1][r] >> 8;
+                        const uint32_t k0[4] = {low(kw[0][r]), low(kw[1][r]), high(kw[0][r]), high(kw[1][r])};
+                        const uint32_t k1[4] = {low(x), low(y), high(x), high(y)};
+                        if (kv == 0)
+                            mma16816_first(a[r], k0[0], k0[1], k0[2], k0[3], qb[kv][0][r][0], qb[kv][0][r][1]);
+                        else
+                            mma16816(a[r], k0[0], k0[1], k0[2], k0[3], qb[kv][0][r][0], qb[kv][0][r][1]);
+                        mma16816(a[r], k1[0], k1[1], k1[2], k1[3], qb[kv][0][r][2], qb[kv][0][r][3]);
+                        if constexpr (F32) {
+                            float lower[4];
+                            mma16816_first(lower, k0[0], k0[1], k0[2], k0[3], qb[kv][1][r][0], qb[kv][1][r][1]);
+                            mma16816(lower, k1[0], k1[1], k1[2], k1[3], qb[kv][1][r][2], qb[kv][1][r][3]);
 #pragma unroll
-                        for (int h = NQ - 1; h >= 0; --h) {  // the small part first
-                            if (kv == 0 && h == NQ - 1)
-                                mma16816_first(a[r], kw[0][r] & kLowNibbles, kw[1][r] & kLowNibbles,
-                                               kw[0][r] & kHighNibbles, kw[1][r] & kHighNibbles, qb[kv][h][r][0],
-                                               qb[kv][h][r][1]);
-                            else
-                                mma16816(a[r], kw[0][r] & kLowNibbles, kw[1][r] & kLowNibbles,
-                                         kw[0][r] & kHighNibbles, kw[1][r] & kHighNibbles, qb[kv][h][r][0],
-                                         qb[kv][h][r][1]);
-                            mma16816(a[r], x & kLowNibbles, y & kLowNibbles, x & kHighNibbles, y & kHighNibbles,
-                                     qb[kv][h][r][2], qb[kv][h][r][3]);
+                            for (int e = 0; e < 4; ++e) a[r][e] += lower[e];
                         }
                     }
                 }
@@ -702,9 +746,9 @@ __global__ void __launch_bounds__(Cfg4<T, D, NREP, KVH>::THREADS, 1) decode4_ker
                     float2 s0 = make_float2(0.f, 0.f);
 #pragma unroll
                     for (int r = 0; r < NG; ++r) {
-                        const float s = __uint_as_float(kp[r] & 0xFFFF0000u), m = __uint_as_float(kp[r] << 16);
-                        s0 = __ffma2_rn(make_float2(s, s), make_float2(a[r][2 * h], a[r][2 * h + 1]), s0);
-                        s0 = __ffma2_rn(make_float2(m, m), qsum[r], s0);
+                        const float2 sm = scale_and_zero<F32>(kp[r]);
+                        s0 = __ffma2_rn(make_float2(sm.x, sm.x), make_float2(a[r][2 * h], a[r][2 * h + 1]), s0);
+                        s0 = __ffma2_rn(make_float2(sm.y, sm.y), qsum[r], s0);
                     }
                     sc[2 * j + h] = s0;
                 }
@@ -743,7 +787,7 @@ __global__ void __launch_bounds__(Cfg4<T, D, NREP, KVH>::THREADS, 1) decode4_ker
                 vtop = __reduce_max_sync(kFull, vtop);
                 st.ref.x = fmaxf(st.ref.x, top.x);
                 st.ref.y = fmaxf(st.ref.y, top.y);
-                st.limit = make_float2((st.ref.x + kSlack) / fac2.x, (st.ref.y + kSlack) / fac2.y);
+                st.limit = make_float2((st.ref.x + kSlack<F32>) / fac2.x, (st.ref.y + kSlack<F32>) / fac2.y);
                 st.vexp = max(st.vexp, int(vtop >> 23) - 127);
                 const float de = float(old_exp - st.vexp);
                 const float2 al = make_float2(fast_exp2_approx(old.x - st.ref.x + de),
@@ -765,9 +809,9 @@ __global__ void __launch_bounds__(Cfg4<T, D, NREP, KVH>::THREADS, 1) decode4_ker
             // ---- weights, and their products with V ----
             // fp32 calls take the power of two after the exponential: the argument is then near
             // 0 for the largest weights, and its rounding with it
-            const float shift = F32 ? 0.0f : float(kHead - st.vexp);
+            const float shift = F32 ? 0.0f : float(kHead<F32> - st.vexp);
             const float2 off = make_float2(shift - st.ref.x, shift - st.ref.y);
-            const float after = pow2f(min(kHead - st.vexp, 127));
+            const float after = pow2f(min(kHead<F32> - st.vexp, 127));
 #pragma unroll
             for (int j = 0; j < NM; ++j) {
                 float2 pr[2];
@@ -793,13 +837,14 @@ __global__ void __launch_bounds__(Cfg4<T, D, NREP, KVH>::THREADS, 1) decode4_ker
                     uint32_t pb[NQ][2];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const float s = __uint_as_float(vpar[2 * j + h][r] & 0xFFFF0000u);
-                        const float m = __uint_as_float(vpar[2 * j + h][r] << 16);
-                        float2 ps = __fmul2_rn(pr[h], make_float2(s, s));
-                        st.om[r] = __ffma2_rn(pr[h], make_float2(m, m), st.om[r]);
+                        const float2 sm = scale_and_zero<F32>(vpar[2 * j + h][r]);
+                        float2 ps = __fmul2_rn(pr[h], make_float2(sm.x, sm.x));
+                        st.om[r] = __ffma2_rn(pr[h], make_float2(sm.y, sm.y), st.om[r]);
 #pragma unroll
                         for (int q = 0; q < NQ; ++q) {
-                            const uint32_t hp = half2_bits(ps.x, ps.y);
+                            // fp32, the upper part: a multiple of 2^3 below 2^14
+                            const uint32_t hp = F32 && q == 0 ? half2_bits(to_multiple<3>(ps.x), to_multiple<3>(ps.y))
+                                                              : half2_bits(ps.x, ps.y);
                             pb[q][h] = transpose8x8(hp);
                             const float2 part = half2_floats(hp);
                             ps = make_float2(ps.x - part.x, ps.y - part.y);
@@ -810,14 +855,24 @@ __global__ void __launch_bounds__(Cfg4<T, D, NREP, KVH>::THREADS, 1) decode4_ker
                         const uint32_t x = __byte_perm(vw[kv][0][r], vw[kv][1][r], half_sel);
                         const uint32_t y = __byte_perm(vw[kv][2][r], vw[kv][3][r], half_sel);
                         const uint32_t xs = x >> 8, ys = y >> 8;
+                        const uint32_t v0[4] = {low(x), high(x), low(y), high(y)};
+                        const uint32_t v1[4] = {low(xs), high(xs), low(ys), high(ys)};
+                        if constexpr (F32) {
+                            float o[2][2][4];  // upper and lower part of P'
 #pragma unroll
-                        for (int q = 0; q < NQ; ++q) {
-                            const uint32_t b0 = KVH == 1 ? pb[q][0] : half2_times(pb[q][0], keep[kv]);
-                            const uint32_t b1 = KVH == 1 ? pb[q][1] : half2_times(pb[q][1], keep[kv]);
-                            mma16816(st.o[r][0], x & kLowNibbles, x & kHighNibbles, y & kLowNibbles,
-                                     y & kHighNibbles, b0, b1);
-                            mma16816(st.o[r][1], xs & kLowNibbles, xs & kHighNibbles, ys & kLowNibbles,
-                                     ys & kHighNibbles, b0, b1);
+                            for (int q = 0; q < 2; ++q) {
+                                mma16816_first(o[q][0], v0[0], v0[1], v0[2], v0[3], pb[q][0], pb[q][1]);
+                                mma16816_first(o[q][1], v1[0], v1[1], v1[2], v1[3], pb[q][0], pb[q][1]);
+                            }
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) st.o[r][i][e] += o[0][i][e] + o[1][i][e];
+                        } else {
+                            const uint32_t b0 = KVH == 1 ? pb[0][0] : half2_times(pb[0][0], keep[kv]);
+                            const uint32_t b1 = KVH == 1 ? pb[0][1] : half2_times(pb[0][1], keep[kv]);
+                            mma16816(st.o[r][0], v0[0], v0[1], v0[2], v0[3], b0, b1);
+                            mma16816(st.o[r][1], v1[0], v1[1], v1[2], v1[3], b0, b1);
                         }
                     }
                 }
@@ -848,7 +903,7 @@ __global__ void __launch_bounds__(Cfg4<T, D, NREP, KVH>::THREADS, 1) decode4_ker
         // column 2 t4 + e is head h_of(e) of the unit, if it is one
         auto h_of = [&](int e) { return KVH == 1 ? 2 * t4 + e : (t4 >> 1) * NREP + ((2 * t4 + e) & 3); };
         auto is_head = [&](int e) { return KVH == 1 ? 2 * t4 + e < NREP : ((2 * t4 + e) & 3) < NREP; };
-        const float mshift = float(st.vexp - kHead);
+        const float mshift = float(st.vexp - kHead<F32>);
         const float m_own[2] = {last < 0 ? -INFINITY : st.ref.x + mshift, last < 0 ? -INFINITY : st.ref.y + mshift};
         if (g8 == 0) {
 #pragma unroll
@@ -869,7 +924,7 @@ __global__ void __launch_bounds__(Cfg4<T, D, NREP, KVH>::THREADS, 1) decode4_ker
                 for (int i = 0; i < NWARPS / 4; ++i)
                     M = fmaxf(fmaxf(M, fmaxf(ms[i].x, ms[i].y)), fmaxf(ms[i].z, ms[i].w));
                 const float f = last < 0 ? 0.0f : fast_exp2_approx(m_own[e] - M);  // M >= m_own > -inf
-                const float f24 = f * 16777216.0f, f20 = f * 1048576.0f;           // even / odd nibbles
+                const float f24 = f * (F32 ? 1.0f : 16777216.0f), f20 = f24 * 0.0625f;  // even / odd nibbles
                 if (g8 == 0) warp_l[h * NWARPS + warp] = last < 0 ? 0.0f : (e ? st.l.y : st.l.x) * f;
                 if (last < 0) continue;  // the slots hold tiles of the next unit
 #pragma unroll
