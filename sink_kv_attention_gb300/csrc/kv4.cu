@@ -21,33 +21,50 @@ template <> struct Out8<float> {
     }
 };
 
-// One thread per word of 8 codes (D / 8 words of K, then D / 8 of V, per row), in the
-// order of the dims, so that stores are contiguous.
+// A thread has one word of 8 codes of a row (D / 8 words of K, then D / 8 of V, in the order
+// of the dims, so that stores are contiguous) and goes from row to row: kUnroll rows with
+// their loads in flight together, and no index arithmetic but two pointer steps.
+constexpr int kThreads = 256;
+constexpr int kUnroll = 4;
+
 template <typename T, int D>
-__global__ void __launch_bounds__(256) kv4_unpack_kernel(const uint8_t* __restrict__ rows, int64_t n_rows,
-                                                         T* __restrict__ k, T* __restrict__ v) {
-    constexpr int WPH = D / 8;  // words per half
-    const int64_t total = n_rows * 2 * WPH;
-    for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
-         i += int64_t(gridDim.x) * blockDim.x) {
-        const int c = int(i % WPH);
-        const bool is_v = (i / WPH) & 1;
-        const int64_t row = i / (2 * WPH);
-        const uint8_t* half = rows + row * kv4_row_bytes(D) + (is_v ? kv4_half_bytes(D) : 0);
-        const int grp = c / 4, t = c % 4;
-        float f[8];
-        kv4_decode_word(*reinterpret_cast<const uint32_t*>(half + kv4_word_offset(D, t, grp)),
-                        *reinterpret_cast<const uint32_t*>(half + kv4_param_offset(D, grp)), f);
-        Out8<T>::store((is_v ? v : k) + row * D + c * 8, f);
+__global__ void __launch_bounds__(kThreads) kv4_unpack_kernel(const uint8_t* __restrict__ rows, int64_t n_rows,
+                                                              T* __restrict__ k, T* __restrict__ v) {
+    constexpr int WPH = D / 8;                       // words per half
+    constexpr int RPB = kThreads / (2 * WPH);        // rows a block handles at once
+    const int c = threadIdx.x % WPH;
+    const bool is_v = (threadIdx.x / WPH) & 1;
+    const int word_at = (is_v ? kv4_half_bytes(D) : 0) + kv4_word_offset(D, c % 4, c / 4);
+    const int par_at = (is_v ? kv4_half_bytes(D) : 0) + kv4_param_offset(D, c / 4);
+    int64_t row = int64_t(blockIdx.x) * (RPB * kUnroll) + threadIdx.x / (2 * WPH);
+    const int64_t step = int64_t(gridDim.x) * (RPB * kUnroll);
+    const uint8_t* src = rows + row * kv4_row_bytes(D);
+    T* dst = (is_v ? v : k) + row * D + c * 8;
+    for (; row < n_rows; row += step, src += step * kv4_row_bytes(D), dst += step * D) {
+        uint32_t word[kUnroll], par[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            if (row + u * RPB >= n_rows) break;
+            word[u] = __ldcs(reinterpret_cast<const uint32_t*>(src + u * RPB * kv4_row_bytes(D) + word_at));
+            par[u] = __ldcs(reinterpret_cast<const uint32_t*>(src + u * RPB * kv4_row_bytes(D) + par_at));
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            if (row + u * RPB >= n_rows) break;
+            float f[8];
+            kv4_decode_word(word[u], par[u], f);
+            Out8<T>::store(dst + u * RPB * D, f);
+        }
     }
 }
 
 template <typename T, int D>
 cudaError_t launch_unpack(const void* rows, int64_t n_rows, void* k, void* v, cudaStream_t st) {
-    const int64_t threads = n_rows * (D / 4);
-    const int64_t blocks = std::min<int64_t>((threads + 255) / 256, int64_t(device_sm_count()) * 32);
-    kv4_unpack_kernel<T, D><<<unsigned(blocks), 256, 0, st>>>(static_cast<const uint8_t*>(rows), n_rows,
-                                                              static_cast<T*>(k), static_cast<T*>(v));
+    constexpr int rows_per_block = kThreads / (D / 4) * kUnroll;
+    const int64_t blocks = std::min<int64_t>((n_rows + rows_per_block - 1) / rows_per_block,
+                                             int64_t(device_sm_count()) * 16);
+    kv4_unpack_kernel<T, D><<<unsigned(blocks), kThreads, 0, st>>>(static_cast<const uint8_t*>(rows), n_rows,
+                                                                   static_cast<T*>(k), static_cast<T*>(v));
     return cudaGetLastError();
 }
 

@@ -50,8 +50,8 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return y;
 }
 
-// x / d for a divisor whose reciprocal is held in two parts, inv + lo = 1/d to 2^-47: one
-// rounding of a product that is off by 2^-47, so the quotient is the correctly rounded one
+// x / d for a divisor whose reciprocal is held in two parts, inv + lo = 1/d to 2^-46: one
+// rounding of a product that is off by 2^-46, so the quotient is the correctly rounded one
 // unless x / d is that close to the middle of two floats, and exact where x / d is a float
 // (the ties of rint, and quotients that are bf16 values, among them).
 __device__ __forceinline__ float div_by(float x, float inv, float lo) { return fmaf(x, inv, x * lo); }
@@ -82,7 +82,8 @@ template <int N>
 __device__ __forceinline__ uint32_t kv4_codes(const float* x, float m, float s) {
     uint32_t w = 0;
     if (s >= 7.9e-31f && s <= 1.2e27f) {  // 2^-100, 2^90: no part of 1/s underflows
-        const float inv = __frcp_rn(s);
+        float inv;  // to 1 ulp; with lo = (1 - s inv) inv the two parts are 1/s to 2^-46
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
         const float lo = fmaf(-s, inv, 1.0f) * inv;
         const float2 m2 = make_float2(-m, -m), inv2 = make_float2(inv, inv), lo2 = make_float2(lo, lo);
         const float2 magic = make_float2(12582912.0f, 12582912.0f);
@@ -100,11 +101,24 @@ __device__ __forceinline__ uint32_t kv4_codes(const float* x, float m, float s) 
     return w;
 }
 
-// The 8 values of a word.
+// The 8 values of a word.  A nibble masked in place under the exponent of 2^23 is 2^23 +
+// code * 16^i, exactly, for i < 4; the power of 16 goes into the scale.
 __device__ __forceinline__ void kv4_decode_word(uint32_t w, uint32_t param, float* f) {
     const float m = __uint_as_float(param << 16), s = __uint_as_float(param & 0xFFFF0000u);
+    const float2 m2 = make_float2(m, m), bias = make_float2(-8388608.0f, -8388608.0f);
+    const float2 s01 = make_float2(s, s * 0.0625f), s23 = make_float2(s * 0.00390625f, s * 0.000244140625f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = fmaf(float((w >> (4 * i)) & 15u), s, m);
+    for (int h = 0; h < 2; ++h, w >>= 16) {
+        const float2 c01 = __fadd2_rn(make_float2(__uint_as_float((w & 0x000Fu) | 0x4B000000u),
+                                                  __uint_as_float((w & 0x00F0u) | 0x4B000000u)), bias);
+        const float2 c23 = __fadd2_rn(make_float2(__uint_as_float((w & 0x0F00u) | 0x4B000000u),
+                                                  __uint_as_float((w & 0xF000u) | 0x4B000000u)), bias);
+        const float2 a = __ffma2_rn(c01, s01, m2), b = __ffma2_rn(c23, s23, m2);
+        f[4 * h] = a.x;
+        f[4 * h + 1] = a.y;
+        f[4 * h + 2] = b.x;
+        f[4 * h + 3] = b.y;
+    }
 }
 
 }  // namespace sk

@@ -213,24 +213,38 @@ template <> struct CacheStore<__nv_bfloat16> {
 };
 
 // This lane's part of a 4-bit row half: x holds dims c VEC .. c VEC + VEC - 1 of the row
-// (c = lane within the row), `half` points at the half's bytes.  The lanes of a group of
+// (c = lane within the row; `raw` the same as it is stored), `half` points at the half's bytes.  The lanes of a group of
 // 32 dims find its extremes by shuffle (every lane of the warp must call this), each
 // quantises its own values, and one word of 8 codes is stored per 8 dims: by each lane
 // for bf16 rows, by the even lane of a pair for fp32 rows.
 template <typename IO, int D>
-__device__ __forceinline__ void kv4_store(uint8_t* half, const float* x, int c, bool store) {
+__device__ __forceinline__ void kv4_store(uint8_t* half, const uint4& raw, const float* x, int c, bool store) {
     constexpr int VEC = RowLayout<IO, D>::VEC;
     constexpr int LPG = 32 / VEC;  // lanes per group
-    float lo = x[0], hi = x[0];
+    float lo, hi;
+    if constexpr (VEC == 8) {
+        // bf16 rows: extremes of packed pairs, then of (smallest, -largest) as one pair
+        const __nv_bfloat162* w = reinterpret_cast<const __nv_bfloat162*>(&raw);
+        const __nv_bfloat162 mn = __hmin2_nan(__hmin2_nan(w[0], w[1]), __hmin2_nan(w[2], w[3]));
+        const __nv_bfloat162 mx = __hmax2_nan(__hmax2_nan(w[0], w[1]), __hmax2_nan(w[2], w[3]));
+        const __nv_bfloat162 neg = __hneg2(mx);
+        __nv_bfloat162 e = __hmin2_nan(__lows2bfloat162(mn, neg), __highs2bfloat162(mn, neg));
 #pragma unroll
-    for (int i = 1; i < VEC; ++i) {
-        lo = min_nan(lo, x[i]);
-        hi = max_nan(hi, x[i]);
-    }
+        for (int o = LPG / 2; o > 0; o >>= 1) e = __hmin2_nan(e, __shfl_xor_sync(kFull, e, o));
+        lo = __low2float(e);
+        hi = -__high2float(e);
+    } else {
+        lo = hi = x[0];
 #pragma unroll
-    for (int o = LPG / 2; o > 0; o >>= 1) {
-        lo = min_nan(lo, __shfl_xor_sync(kFull, lo, o));
-        hi = max_nan(hi, __shfl_xor_sync(kFull, hi, o));
+        for (int i = 1; i < VEC; ++i) {
+            lo = min_nan(lo, x[i]);
+            hi = max_nan(hi, x[i]);
+        }
+#pragma unroll
+        for (int o = LPG / 2; o > 0; o >>= 1) {
+            lo = min_nan(lo, __shfl_xor_sync(kFull, lo, o));
+            hi = max_nan(hi, __shfl_xor_sync(kFull, hi, o));
+        }
     }
     float m, s;
     kv4_group_params(lo, hi, &m, &s);
@@ -386,7 +400,7 @@ __global__ void __launch_bounds__(kThreads + 32) kv_append_kernel(AppendParams p
                         ElemIO<IO>::unpack(out, f);
                         uint8_t* half = static_cast<uint8_t*>(p.kc) + crow * kv4_row_bytes(D) +
                                         (which == 2 ? kv4_half_bytes(D) : 0);
-                        kv4_store<IO, D>(half, f, c, store_kv);
+                        kv4_store<IO, D>(half, out, f, c, store_kv);
                     }
                 } else if constexpr (sizeof(KC) == 1) {
                     // int8 K: symmetric absmax over the row, codes rint(x * 127 / max|x|), ties to even.
