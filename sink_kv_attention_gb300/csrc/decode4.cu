@@ -192,35 +192,31 @@ __device__ __forceinline__ int64_t div_rows(int64_t a, int64_t b) {  // a, b >= 
     return ((a | b) >> 32) == 0 ? int64_t(uint32_t(a) / uint32_t(b)) : a / b;
 }
 
-// The rows of the batch in shared memory: len[b] visible rows of a unit of sequence b, and
-// start[b] = Hu * (len[0] + .. + len[b - 1]), the first row of its first unit; Hu units a
-// sequence.
+// The rows of the batch in shared memory.  The split counts `extra` rows more for each unit,
+// in front of its own: taking up a unit and merging its warps costs a block about as much as
+// those rows would, and a share of short units would otherwise take several times as long as
+// one of long ones (ragged 16-token pages: measured 51.7 us without).
 struct Rows4 {
-    int64_t* start;  // [B + 1]
-    int64_t* len;    // [B]
+    int64_t* start;  // [B + 1] counted rows before sequence b: Hu units of len + extra each
+    int64_t* len;    // [B] visible rows of a unit of sequence b
     int64_t* shift;  // [B] paged: rows behind the sinks hold key row + shift (0: every row its key)
+    int extra;
 };
 
-// The units of a share, in order.  A share has fewer than 2^31 rows (its rows are bytes of
-// HBM), so offsets into it are 32 bits.
+// The units of a share of counted rows, in order, as far as they have rows of their own in
+// it.  A share has fewer than 2^31 rows (its rows are bytes of HBM), so offsets into it are 32
+// bits.
 struct Units4 {
     int b, g;     // sequence, unit of the sequence
     int rows;     // the unit's rows in the share
-    int rest;     // the share's rows behind them
+    int rest;     // counted rows of the share behind them
     int64_t r0;   // the unit's first row in the share
-    __device__ __forceinline__ void begin(const Rows4& rw, int B, int64_t lo, int64_t hi) {
-        int l = 0, h = B;  // largest b with start[b] <= lo < start[b + 1]
-        while (h - l > 1) {
-            const int m = (l + h) >> 1;
-            if (rw.start[m] <= lo) l = m; else h = m;
-        }
-        b = l;
-        const int64_t len = rw.len[b], off = lo - rw.start[b];
-        g = int(div_rows(off, len));
-        r0 = off - g * len;
-        rest = int(hi - lo);
-        rows = int(min(int64_t(rest), len - r0));
-        rest -= rows;
+    __device__ __forceinline__ void take(const Rows4& rw, int64_t from) {  // from: counted rows of it before the share
+        const int64_t counted = rw.len[b] + rw.extra;
+        const int64_t to = min(counted, from + rest);
+        rest -= int(to - from);
+        r0 = max(int64_t(0), from - rw.extra);
+        rows = int(max(int64_t(0), to - rw.extra - r0));
     }
     // the next unit of the share; false: there is none
     __device__ __forceinline__ bool next(const Rows4& rw, int Hu) {
@@ -229,10 +225,21 @@ struct Units4 {
             g = 0;
             do { ++b; } while (rw.len[b] == 0);  // rows are left, so a sequence with rows is
         }
-        r0 = 0;
-        rows = int(min(int64_t(rest), rw.len[b]));
-        rest -= rows;
-        return true;
+        take(rw, 0);
+        return rows > 0;
+    }
+    __device__ __forceinline__ void begin(const Rows4& rw, int B, int Hu, int64_t lo, int64_t hi) {
+        int l = 0, h = B;  // largest b with start[b] <= lo < start[b + 1]
+        while (h - l > 1) {
+            const int m = (l + h) >> 1;
+            if (rw.start[m] <= lo) l = m; else h = m;
+        }
+        b = l;
+        const int64_t counted = rw.len[b] + rw.extra, off = lo - rw.start[b];
+        g = int(div_rows(off, counted));
+        rest = int(hi - lo);
+        take(rw, off - g * counted);
+        if (rows == 0) next(rw, Hu);  // the share has a row: it is longer than `extra`
     }
 };
 
@@ -253,8 +260,8 @@ struct TileWalk {
         at = (warp >= warp0 ? warp - warp0 : warp + NWARPS - warp0) * TR - lead(rows);
         left = u.rows - at;
     }
-    __device__ __forceinline__ void begin(const Rows4& rows, int B, int64_t lo, int64_t hi, int warp) {
-        u.begin(rows, B, lo, hi);
+    __device__ __forceinline__ void begin(const Rows4& rows, int B, int Hu, int64_t lo, int64_t hi, int warp) {
+        u.begin(rows, B, Hu, lo, hi);
         warp0 = 0;
         unit(rows, warp);
     }
@@ -487,9 +494,9 @@ __global__ void __launch_bounds__(Cfg4<T, D, NREP, KVH>::THREADS, 1) decode4_ker
     uint64_t* bars = all_bars + warp * SLOTS;
     uint64_t* q_bars = all_bars + NWARPS * SLOTS;
     uint8_t* ring = smem + size_t(warp) * SLOTS * C::SLOT_BYTES;
-    const Rows4 rows{reinterpret_cast<int64_t*>(smem + C::OFF_ROWS),
+    Rows4 rows{reinterpret_cast<int64_t*>(smem + C::OFF_ROWS),
                      reinterpret_cast<int64_t*>(smem + C::OFF_ROWS) + kMaxBatch + 1,
-                     reinterpret_cast<int64_t*>(smem + C::OFF_ROWS) + 2 * kMaxBatch + 1};
+                     reinterpret_cast<int64_t*>(smem + C::OFF_ROWS) + 2 * kMaxBatch + 1, 0};
     float* warp_m = reinterpret_cast<float*>(smem + C::OFF_M);  // [HEADS][NWARPS] references
     float* warp_l = warp_m + HEADS * NWARPS;                    // [HEADS][NWARPS] sums, at the block's reference
     int* warp_slot = reinterpret_cast<int*>(smem + C::OFF_FLAGS);  // [NWARPS] where a warp's sums are; -1: none
@@ -532,7 +539,7 @@ __global__ void __launch_bounds__(Cfg4<T, D, NREP, KVH>::THREADS, 1) decode4_ker
             }
         }
         if (!__syncthreads_or(changed)) break;
-        if (warp == 0) {  // scan
+        if (warp == 0) {  // rows before each sequence, uncounted extras left out for now
             int64_t carry = 0;
             for (int b0 = 0; b0 < p.B; b0 += 32) {
                 const int b = b0 + lane;
@@ -548,16 +555,31 @@ __global__ void __launch_bounds__(Cfg4<T, D, NREP, KVH>::THREADS, 1) decode4_ker
             if (lane == 0) rows.start[0] = 0;
         }
         __syncthreads();
-        // Blocks that take part: enough for one tile a warp, or one unit each if that is more
-        // (every block of them has a row).
+        // Blocks that take part: enough for one tile a warp, or one unit each if that is more.
         R = rows.start[p.B];
         P = int(min(int64_t(gridDim.x), max(min(units, R), R / (NWARPS * TR))));
         // Units of one length that nearly fill the GPU: one to a block, nothing is cut (measured on
         // 128 units of 4096 rows over 152 SMs: 41.4 -> 36.7 us, the stream alone the same).
         if (units <= gridDim.x && units * 4 >= int64_t(gridDim.x) * 3 && R == units * rows.len[0]) P = int(units);
-        if (c < P) {
-            w.begin(rows, p.B, div_rows(int64_t(c) * R + P - 1, P), div_rows(int64_t(c + 1) * R + P - 1, P), warp);
+        // at most half a share, so that every share has rows of its own
+        rows.extra = P > 0 ? int(min(int64_t(2 * NWARPS * TR), div_rows(R, P) / 2)) : 0;
+        __syncthreads();  // every thread has R
+        if (warp == 0) {
+            int before = 0;  // sequences with rows
+            for (int b0 = 0; b0 < p.B; b0 += 32) {
+                const int b = b0 + lane;
+                const uint32_t m = __ballot_sync(kFull, b < p.B && rows.len[b] > 0);
+                if (b < p.B)
+                    rows.start[b + 1] += int64_t(p.Hkv) * rows.extra *
+                                         (before + __popc(m & (0xffffffffu >> (31 - lane))));
+                before += __popc(m);
+            }
         }
+        __syncthreads();
+        R = rows.start[p.B];  // counted rows from here on
+        if (c < P)
+            w.begin(rows, p.B, p.Hkv, div_rows(int64_t(c) * R + P - 1, P), div_rows(int64_t(c + 1) * R + P - 1, P),
+                    warp);
     }
 
     // sequences with nothing visible: zeros, each from one block
@@ -973,11 +995,12 @@ __global__ void __launch_bounds__(Cfg4<T, D, NREP, KVH>::THREADS, 1) decode4_ker
         }
         if (!whole) {  // a share has two cut units at most: its first and its last
             if (threadIdx.x == 0) {
-                const int64_t len = rows.len[w.u.b], start = rows.start[w.u.b] + w.u.g * len;
-                const int64_t from = div_rows(start * P, R);  // the unit's blocks: from, from + 1, ..
+                const int64_t counted = rows.len[w.u.b] + rows.extra;
+                const int64_t start = rows.start[w.u.b] + w.u.g * counted;
+                const int64_t from = div_rows((start + rows.extra) * P, R);  // the unit's blocks: from, from + 1, ..
                 cuts[n_cuts].unit = unit;
                 cuts[n_cuts].first = unit + from;
-                cuts[n_cuts].n = int(div_rows((start + len - 1) * P, R) - from) + 1;
+                cuts[n_cuts].n = int(div_rows((start + counted - 1) * P, R) - from) + 1;
             }
             ++n_cuts;
         }
