@@ -45,12 +45,13 @@
 // through the ring slot that its warp has just emptied.
 //
 // One kernel: a block that holds all of a unit writes its output; a unit cut between blocks
-// is finished by whichever of them is last to write its partial (softmax states in the
-// workspace, added in the blocks' order, so the result does not depend on who is last).
-// The count of partials of a unit is a word of the workspace tagged with a number that is
-// this launch's own, so the workspace needs no initialisation: a word with another tag
-// counts as 0, and the last block writes it back to 0 (a graph replays its launch with the
-// same tag).  Nothing waits for another block.
+// is finished by whichever of them finds every partial written when it has written its own
+// (softmax states in the workspace, added in the blocks' order, so the result does not depend
+// on who that is, and two that find it so write the same bits).  A partial is marked by a word
+// that holds a number of this launch's own, so the workspace needs no initialisation; who
+// finishes a unit takes its marks back (a graph replays its launch with the same number).
+// Nothing waits for another block, and there is no counter for the blocks to queue at (a
+// compare-and-swap counter took 0.35 us for each block of a unit).
 //
 // Rows are visited in an order that spreads a quarter warp's 16-byte loads over all
 // banks: matrix row r of a 16-row tile is key kappa(r), chosen so that (0,1), (2,3), ..
@@ -81,7 +82,7 @@ constexpr uint32_t kLowNibbles = 0x000F000Fu, kHighNibbles = 0x00F000F0u;
 // A unit of a block that other blocks share.
 struct Cut4 {
     int64_t unit, first;  // the unit and the workspace slot of its first partial
-    int n, last;          // its partials; whether this block was the last to count one
+    int n, own;           // its partials, and which of them is this block's
 };
 
 // KVH kv heads share a block's unit: their q heads are columns 4 kv .. 4 kv + NREP - 1 of
@@ -107,8 +108,8 @@ template <typename T, int D, int NREP, int KVH> struct Cfg4 {
     static constexpr size_t SMEM = OFF_FLAGS + NWARPS * 4 + 2 * sizeof(Cut4);
     static constexpr int THREADS = NWARPS * 32;
     static_assert(HEADS * D * 4 <= SLOT_BYTES, "a slot holds a warp's sums");
-    // workspace: a counter per unit, then the partials
-    __host__ __device__ static constexpr int64_t ws_counter_floats(int64_t units) { return (units + 1) / 2 * 4; }
+    // workspace: a mark per partial, then the partials (a slot for each unit and block)
+    __host__ __device__ static constexpr int64_t marks_floats(int64_t slots) { return (slots + 1) / 2 * 4; }
     static_assert(KVH == 1 || (KVH == 2 && NREP <= 4), "columns");
     static_assert(OFF_Q % 16 == 0 && OFF_BAR % 16 == 0 && OFF_M % 16 == 0 && NWARPS % 4 == 0, "alignment");
     static_assert(SMEM <= 232448, "shared memory");
@@ -466,17 +467,17 @@ __device__ __noinline__ void combine_unit(const DecodeParams& p, int64_t unit, c
     __syncthreads();
 }
 
-// Counts one of a unit's n partials; true for the last.  The word holds the launch's tag
-// (48 bits) and the count.
-__device__ __forceinline__ bool count_partial(unsigned long long* word, uint64_t tag, int n) {
-    unsigned long long seen = 0;  // as a finished call leaves it
-    while (true) {
-        const unsigned long long now = (seen >> 16) == tag ? seen + 1 : ((tag << 16) | 1ull);
-        const bool all = int(now & 0xFFFF) == n;
-        const unsigned long long was = atomicCAS(word, seen, all ? 0ull : now);
-        if (was == seen) return all;
-        seen = was;
-    }
+// Marks a unit's partial `own` as written (the warp; its block's threads have all passed a
+// fence and a barrier since they wrote it) and tells whether all n are.  Of the blocks that
+// mark theirs, the last in the order of the fences sees all.
+__device__ __forceinline__ bool mark_partial(uint64_t* marks, int own, int n, uint64_t tag, int lane) {
+    volatile uint64_t* m = marks;
+    if (lane == 0) m[own] = tag;
+    __syncwarp();
+    __threadfence();
+    bool all = true;
+    for (int i = lane; i < n; i += 32) all = all && m[i] == tag;
+    return __all_sync(kFull, all);
 }
 
 template <typename T, int D, int NREP, int KVH, bool PAGED>
@@ -558,11 +559,21 @@ __global__ void __launch_bounds__(Cfg4<T, D, NREP, KVH>::THREADS, 1) decode4_ker
         // Blocks that take part: enough for one tile a warp, or one unit each if that is more.
         R = rows.start[p.B];
         P = int(min(int64_t(gridDim.x), max(min(units, R), R / (NWARPS * TR))));
-        // Units of one length that nearly fill the GPU: one to a block, nothing is cut (measured on
-        // 128 units of 4096 rows over 152 SMs: 41.4 -> 36.7 us, the stream alone the same).
-        if (units <= gridDim.x && units * 4 >= int64_t(gridDim.x) * 3 && R == units * rows.len[0]) P = int(units);
+        // Units of one length: the same number of blocks for each, so that no block has parts of
+        // two, unless that leaves more than a quarter (one block each) or an eighth of the GPU's
+        // blocks idle.  Measured: 128 units of 4096 rows over 152 SMs 41.4 -> 36.7 us (the stream
+        // alone the same), 4 of 4096 17.1 -> 12.8, 16 of 4096 17.1 -> 14.3.
+        bool even = false;
+        if (R > 0 && units <= gridDim.x && R == units * rows.len[0]) {
+            const int n = int(units), grid = int(gridDim.x);
+            const int up = (P + n - 1) / n * n, down = P / n * n;
+            if (n * 4 >= grid * 3) P = n;
+            else if (up <= grid) P = up;
+            else if ((grid - down) * 8 <= grid) P = down;
+            even = P % n == 0;
+        }
         // at most half a share, so that every share has rows of its own
-        rows.extra = P > 0 ? int(min(int64_t(2 * NWARPS * TR), div_rows(R, P) / 2)) : 0;
+        rows.extra = P > 0 && !even ? int(min(int64_t(2 * NWARPS * TR), div_rows(R, P) / 2)) : 0;
         __syncthreads();  // every thread has R
         if (warp == 0) {
             int before = 0;  // sequences with rows
@@ -604,7 +615,8 @@ __global__ void __launch_bounds__(Cfg4<T, D, NREP, KVH>::THREADS, 1) decode4_ker
     }
     int q_at = 0;
     uint32_t q_phase = 0;
-    float* partials = p.ws + C::ws_counter_floats(units);
+    uint64_t* marks = reinterpret_cast<uint64_t*>(p.ws);
+    float* partials = p.ws + C::marks_floats(units + gridDim.x);
     int n_cuts = 0;
     Loader<C, KVH, PAGED> ld;
     ld.t = w;
@@ -1000,6 +1012,7 @@ __global__ void __launch_bounds__(Cfg4<T, D, NREP, KVH>::THREADS, 1) decode4_ker
                 const int64_t from = div_rows((start + rows.extra) * P, R);  // the unit's blocks: from, from + 1, ..
                 cuts[n_cuts].unit = unit;
                 cuts[n_cuts].first = unit + from;
+                cuts[n_cuts].own = int(c - from);
                 cuts[n_cuts].n = int(div_rows((start + counted - 1) * P, R) - from) + 1;
             }
             ++n_cuts;
@@ -1015,13 +1028,14 @@ __global__ void __launch_bounds__(Cfg4<T, D, NREP, KVH>::THREADS, 1) decode4_ker
         if (++q_at == 2) { q_at = 0; q_phase ^= 1; }
     } while (w.next_unit(rows, p.Hkv, warp));
 
-    // ---- the cut units: count this block's partials, and finish the units that are now whole ----
+    // ---- the cut units: mark this block's partials, and finish the units that are now whole ----
     if (n_cuts > 0) {
-        __threadfence();  // the partials are visible before they are counted
+        __threadfence();  // the partials are visible before their marks
         __syncthreads();
-        if (threadIdx.x < n_cuts) {
-            Cut4& cut = cuts[threadIdx.x];
-            cut.last = count_partial(reinterpret_cast<unsigned long long*>(p.ws) + cut.unit, tag, cut.n) ? 1 : 0;
+        if (warp < n_cuts) {
+            const Cut4 cut = cuts[warp];
+            const bool all = mark_partial(marks + cut.first, cut.own, cut.n, tag, lane);
+            if (lane == 0) warp_slot[warp] = all;
         }
         __syncthreads();
         __threadfence();
@@ -1029,23 +1043,25 @@ __global__ void __launch_bounds__(Cfg4<T, D, NREP, KVH>::THREADS, 1) decode4_ker
 #pragma unroll 1
         for (int i = 0; i < n_cuts; ++i) {
             const Cut4 cut = cuts[i];
-            if (cut.last)
-                combine_unit<T, D, HEADS, C::PARTIAL_FLOATS, C::THREADS>(
-                    p, cut.unit, partials + cut.first * C::PARTIAL_FLOATS, cut.n, reinterpret_cast<float*>(smem));
+            if (!warp_slot[i]) continue;
+            combine_unit<T, D, HEADS, C::PARTIAL_FLOATS, C::THREADS>(
+                p, cut.unit, partials + cut.first * C::PARTIAL_FLOATS, cut.n, reinterpret_cast<float*>(smem));
+            for (int j = threadIdx.x; j < cut.n; j += C::THREADS) marks[cut.first + j] = 0;
         }
     }
     if (timed_out) set_error(p.err, SK_DEVERR_TIMEOUT);
     if (bad) set_error(p.err, SK_DEVERR_BLOCK_TABLE);
 }
 
-// A 48-bit number that no other launch of this process has, from a random start.
+// A number that no other launch of this process has, never 0, from a start of its own.
 uint64_t launch_tag() {
     static std::atomic<uint64_t> next{[] {
         uint64_t x = uint64_t(std::chrono::system_clock::now().time_since_epoch().count()) ^ (uint64_t(getpid()) << 40);
         x = (x ^ (x >> 30)) * 0xBF58476D1CE4E5B9ull;
         return x ^ (x >> 27);
     }()};
-    return next.fetch_add(1, std::memory_order_relaxed) & 0xFFFFFFFFFFFFull;
+    const uint64_t tag = next.fetch_add(1, std::memory_order_relaxed);
+    return tag != 0 ? tag : next.fetch_add(1, std::memory_order_relaxed);
 }
 
 template <typename T, int D, int NREP, int KVH, bool PAGED>
@@ -1092,13 +1108,11 @@ bool dispatch4(int nrep, const DecodeParams& p, int64_t rows_most, cudaStream_t 
 
 size_t kv4_decode_workspace(int batch, int n_kv_heads, int head_dim, int nrep) {
     if ((head_dim != 64 && head_dim != 128) || (nrep != 1 && nrep != 2 && nrep != 4 && nrep != 8)) return 0;
-    // a counter per unit; a partial per block and unit, of the q heads of up to two kv heads
+    // a mark and a partial for each block and unit; a unit has the q heads of up to two kv heads
     const int pair = nrep <= 4 && n_kv_heads % 2 == 0 ? 2 : 1;
-    const int64_t units = int64_t(batch) * n_kv_heads;
+    const int64_t slots = device_sm_count() + int64_t(batch) * n_kv_heads / pair;
     const int64_t heads = int64_t(nrep) * pair;
-    return size_t((units / pair + 1) / 2 * 4 +
-                  (device_sm_count() + units / pair) * ((heads * (head_dim + 2) + 3) / 4 * 4)) *
-           sizeof(float);
+    return size_t((slots + 1) / 2 * 4 + slots * ((heads * (head_dim + 2) + 3) / 4 * 4)) * sizeof(float);
 }
 
 bool kv4_decode_run(const Kv4DecodeArgs& a, cudaStream_t st, cudaError_t* e) {

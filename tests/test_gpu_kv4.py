@@ -486,6 +486,39 @@ def test_steps_in_a_graph_equal_eager_steps(sk):
     _same_state(a, b)
 
 
+def test_units_cut_between_blocks_in_graphs_that_share_a_workspace(sk):
+    """Sequences long enough to be cut between blocks: two captured calls of other shapes over
+    one workspace, replayed in turn, and eager calls between them, always give the first
+    call's bits (what a call leaves in the workspace never matters to the next)."""
+    D = 128
+    shapes = [(1, 2, 4, 20_000), (3, 3, 8, 7_001)]
+    layers, qs, outs, graphs, want = [], [], [], [], []
+    ws = torch.full((8 << 20,), 0xFF, dtype=torch.uint8, device="cuda")
+    for i, (B, Hkv, rep, n) in enumerate(shapes):
+        a = sk.KVLayer.allocate(sk.SK_LAYER_GLOBAL, B, Hkv, D, capacity=n, bits=4)
+        sk.kv_append(None, a, None, randn((B, n, Hkv, D), 200 + i, BF), randn((B, n, Hkv, D), 210 + i, BF))
+        a.pos.copy_(torch.tensor([n, n - 13, 5][:B]))
+        layers.append(a)
+        qs.append(randn((B, Hkv * rep, D), 220 + i, BF))
+        outs.append(torch.zeros_like(qs[-1]))
+        assert ws.numel() >= sk.decode_workspace_bytes(a, Hkv * rep)
+        want.append(sk.decode_attention(a, qs[i], workspace=ws).clone())
+        ref, A, Bs = attend64(f64(qs[i][0]), a.k[0].cpu().numpy())
+        check(f64(want[i][0]), ref, A, Bs, n, BF)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            sk.decode_attention(a, qs[i], out=outs[i], workspace=ws)
+        graphs.append(g)
+    for r in range(20):
+        for i in (0, 1) if r % 3 else (1, 0, 0):
+            outs[i].zero_()
+            graphs[i].replay()
+            assert torch.equal(outs[i], want[i]), (r, i)
+        if r % 5 == 4:
+            ws.random_(0, 256)
+            assert torch.equal(sk.decode_attention(layers[1], qs[1], workspace=ws), want[1])
+
+
 @pytest.mark.parametrize("kind", ["ring", "global"])
 def test_prefill_over_a_4_bit_prior(sk, kind):
     """A chunk over a 4-bit prior gives the bits of the same chunk over a bf16 cache that
