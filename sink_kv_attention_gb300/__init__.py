@@ -209,7 +209,11 @@ def kv4_row_bytes(head_dim: int) -> int:
 
 def _row_head_dim(k: torch.Tensor) -> int:
     """head_dim of a cache buffer [..., row]: its last size, or that of 4-bit rows."""
-    return k.shape[-1] * 4 // 5 if k.dtype == torch.uint8 else k.shape[-1]
+    if k.dtype != torch.uint8:
+        return k.shape[-1]
+    if k.shape[-1] % 5:
+        raise ValueError("rows are not 4-bit cache rows")
+    return k.shape[-1] // 5 * 4
 
 
 def _need_contig(*ts):
@@ -700,6 +704,10 @@ class PagedGroup:
         self.ref = ref
         for x in self.layers:
             _need_contig(x.k_pool, x.v_pool, x.block_table, x.seq_lens)
+            if x.block_table.dtype != torch.int32 or x.seq_lens.dtype != torch.int64:
+                raise ValueError("block_table must be int32 and seq_lens int64")
+            if x.seq_lens.numel() != x.batch:
+                raise ValueError("seq_lens must hold a length for each request")
         self._structs = (PagedLayerStruct * len(self.layers))(*[x.struct() for x in self.layers])
         self._tensors = [(x.k_pool, x.v_pool, x.block_table, x.sink_block_ids, x.seq_lens, x.err) for x in self.layers]
         need = int(_lib().sk_paged_pages_workspace_bytes(self._structs))
@@ -759,8 +767,6 @@ def kv4_unpack(rows: torch.Tensor, dtype=torch.bfloat16, stream=None):
         raise TypeError("rows must be uint8")
     _need_contig(rows)
     D = _row_head_dim(rows)
-    if rows.shape[-1] != kv4_row_bytes(D):
-        raise ValueError("rows are not 4-bit cache rows")
     K = torch.empty(*rows.shape[:-1], D, dtype=dtype, device=rows.device)
     V = torch.empty_like(K)
     _check(_lib().sk_kv4_unpack(_ptr(rows), rows.numel() // rows.shape[-1], D, _ptr(K), _ptr(V), _sk_dtype(dtype),

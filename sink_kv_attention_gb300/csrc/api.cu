@@ -67,4 +67,4 @@ extern "C" sk_status sk_sync_check(uint32_t* err, int32_t clear, void* stream, u
     return SK_OK;
 }
 
-extern "C" int32_t sk_version(void) { return 200; }
+extern "C" int32_t sk_version(void) { return 300; }

@@ -526,12 +526,22 @@ __global__ void __launch_bounds__(Cfg4<T, D, NREP, KVH>::THREADS, 1) decode4_ker
         if (pass == 1) pdl_wait();  // the append has written the state, q and the new rows
         bool changed = false;
         for (int b = threadIdx.x; b < p.B; b += C::THREADS) {
-            int64_t n = visible_rows(p, b);
-            n = max(int64_t(0), PAGED ? n : min(n, p.cap));
-            int64_t shift = 0;
+            int64_t n, shift = 0;
             if constexpr (PAGED) {
-                const int64_t L = p.pos[b] > 0 ? p.pos[b] + p.sink_len : 0;
-                if (p.W > 0 && L > int64_t(p.S) + p.W) shift = L - p.W - p.S;
+                const int64_t most = int64_t(p.max_blocks) << p.bs_log2;
+                int64_t L = p.pos[b];
+                if (L > most) {  // more tokens than its table names blocks for
+                    if (pass == 1) bad = true;
+                    L = most;
+                }
+                if (L > 0) L += p.sink_len;
+                n = max(int64_t(0), L);
+                if (p.W > 0 && n > int64_t(p.S) + p.W) {
+                    n = int64_t(p.S) + p.W;
+                    shift = L - n;
+                }
+            } else {
+                n = max(int64_t(0), min(visible_rows(p, b), p.cap));
             }
             if (pass == 0 || rows.len[b] != n || (PAGED && rows.shift[b] != shift)) {
                 rows.len[b] = n;
@@ -1108,11 +1118,15 @@ bool dispatch4(int nrep, const DecodeParams& p, int64_t rows_most, cudaStream_t 
 
 size_t kv4_decode_workspace(int batch, int n_kv_heads, int head_dim, int nrep) {
     if ((head_dim != 64 && head_dim != 128) || (nrep != 1 && nrep != 2 && nrep != 4 && nrep != 8)) return 0;
-    // a mark and a partial for each block and unit; a unit has the q heads of up to two kv heads
-    const int pair = nrep <= 4 && n_kv_heads % 2 == 0 ? 2 : 1;
-    const int64_t slots = device_sm_count() + int64_t(batch) * n_kv_heads / pair;
-    const int64_t heads = int64_t(nrep) * pair;
-    return size_t((slots + 1) / 2 * 4 + slots * ((heads * (head_dim + 2) + 3) / 4 * 4)) * sizeof(float);
+    // a mark and a partial for each block and unit; a unit has the q heads of one kv head (fp32
+    // calls always), or of two: room for either
+    size_t most = 0;
+    for (int pair = 1; pair <= (nrep <= 4 && n_kv_heads % 2 == 0 ? 2 : 1); ++pair) {
+        const int64_t slots = device_sm_count() + int64_t(batch) * n_kv_heads / pair;
+        const int64_t heads = int64_t(nrep) * pair;
+        most = std::max(most, size_t((slots + 1) / 2 * 4 + slots * ((heads * (head_dim + 2) + 3) / 4 * 4)));
+    }
+    return most * sizeof(float);
 }
 
 bool kv4_decode_run(const Kv4DecodeArgs& a, cudaStream_t st, cudaError_t* e) {
@@ -1122,7 +1136,7 @@ bool kv4_decode_run(const Kv4DecodeArgs& a, cudaStream_t st, cudaError_t* e) {
     p.out = a.out;
     p.ws = static_cast<float*>(a.ws);
     int D;
-    int64_t rows_most;
+    int64_t unit_rows;  // most rows of a unit
     if (a.paged != nullptr) {
         const sk_paged_layer& L = *a.paged;
         p.kc = L.k_pool;
@@ -1143,7 +1157,7 @@ bool kv4_decode_run(const Kv4DecodeArgs& a, cudaStream_t st, cudaError_t* e) {
         D = L.head_dim;
         int64_t keys = int64_t(L.max_blocks) * L.block_size + p.sink_len;
         if (L.window > 0) keys = std::min<int64_t>(keys, int64_t(L.sinks) + L.window);
-        rows_most = int64_t(L.batch) * L.n_kv_heads * keys;
+        unit_rows = keys;
     } else {
         const sk_kv_layer& L = *a.layer;
         p.kc = L.k;
@@ -1156,8 +1170,11 @@ bool kv4_decode_run(const Kv4DecodeArgs& a, cudaStream_t st, cudaError_t* e) {
         p.S = L.sinks;
         p.kind = L.kind;
         D = L.head_dim;
-        rows_most = int64_t(L.batch) * L.n_kv_heads * L.capacity;
+        unit_rows = L.capacity;
     }
+    // a block's share is counted in 32 bits
+    if (double(p.B) * p.Hkv * double(unit_rows) / device_sm_count() > 1e9) return false;
+    const int64_t rows_most = int64_t(p.B) * p.Hkv * unit_rows;
     p.qscale = kLog2e / sqrtf(float(D));
     if (a.io_dtype == SK_BF16) {
         if (D == 128) return dispatch4<__nv_bfloat16, 128>(a.nrep, p, rows_most, st, e);

@@ -80,6 +80,32 @@ def test_attention_refusals(lib):
     assert lib.sk_paged_decode_workspace_bytes(ctypes.byref(mixed), 32) == 0
 
 
+def test_workspace_holds_either_way_of_pairing_kv_heads(lib):
+    """A slot (a mark of 8 bytes and HEADS (D + 2) floats, padded to 16 bytes) for each unit and
+    block, whether a unit has one kv head (fp32 calls) or two; without a device the block
+    count is 1."""
+    import sink_kv_attention_gb300 as sk
+    for D in (64, 128):
+        for rep in (1, 2, 4, 8):
+            for Hkv in (1, 2, 32):
+                L = _layer(sk, sk.SK_I4, sk.SK_I4, D=D, Hkv=Hkv)
+                L.batch = 1024
+                got = lib.sk_decode_workspace_bytes(ctypes.byref(L), Hkv * rep)
+                for kvh in (1, 2):
+                    if kvh == 2 and (rep > 4 or Hkv % 2):
+                        continue
+                    slots = 1024 * Hkv // kvh + 1
+                    assert got >= slots * 8 + slots * 4 * ((kvh * rep * (D + 2) + 3) // 4 * 4), (D, rep, Hkv, kvh)
+
+
+def test_sizes_past_32_bit_shares_are_refused(lib):
+    import sink_kv_attention_gb300 as sk
+    P = _paged(sk, sk.SK_I4, sk.SK_I4)
+    P.max_blocks, P.block_size = (1 << 31) - 1, 1024
+    assert lib.sk_paged_decode_attention(ctypes.byref(P), A, 32, sk.SK_BF16, None, A, A, 1 << 40, None) == \
+        sk.SK_ERR_UNSUPPORTED
+
+
 def test_other_entry_points_refuse_4_bit_layers(lib):
     """The fused decode step, rerotation and shift have no 4-bit form."""
     import sink_kv_attention_gb300 as sk
@@ -113,6 +139,8 @@ def test_python_checks():
         sk.kv4_unpack(torch.zeros(3, 82, dtype=torch.uint8))
     with pytest.raises(ValueError):
         sk.kv4_unpack(torch.zeros(3, 160, dtype=torch.uint8)[:, ::2])
+    with pytest.raises(ValueError):      # a row that is no 4-bit row
+        sk.KVLayer(sk.SK_LAYER_GLOBAL, torch.zeros(1, 1, 4, 161, dtype=torch.uint8), None, torch.zeros(1).long()).struct()
     L = sk.KVLayer.allocate(sk.SK_LAYER_RING, 2, 3, 128, sinks=1, window=3, device="cpu", bits=4)
     assert L.k.shape == (2, 3, 4, 160) and L.k.dtype == torch.uint8 and L.v is None and L.head_dim == 128
     s = L.struct()

@@ -429,6 +429,54 @@ def test_rows_past_4_gib(sk):
     assert np.all(np.abs(out - want) <= want * (n / (152 * 12 * 8) * 2.0 ** -24 + 2.0 ** -20))
 
 
+@pytest.mark.parametrize("dtype,rep", [(F32, 1), (BF, 1), (BF, 4)])
+def test_a_full_batch_stays_inside_its_workspace(sk, dtype, rep):
+    """1024 sequences of 32 kv heads: the workspace's last slots are used, and nothing behind
+    it; heads far apart agree with float64."""
+    D, B, Hkv, n = 64, 1024, 32, 37
+    a = sk.KVLayer.allocate(sk.SK_LAYER_GLOBAL, B, Hkv, D, capacity=n, bits=4)
+    rows = rows_of((3, Hkv, n), D, 75)
+    a.k.copy_(rows.repeat(B // 3 + 1, 1, 1, 1)[:B])
+    a.pos.copy_(torch.arange(B) * 7 % (n + 1))
+    q = randn((B, Hkv * rep, D), 76, dtype)
+    need = sk.decode_workspace_bytes(a, Hkv * rep)
+    ws = torch.full((need + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
+    out = f64(sk.decode_attention(a, q, workspace=ws[:need]))
+    assert (ws[need:] == 0x5A).all()
+    for b in (0, 1, 500, 1022, 1023):
+        m = b * 7 % (n + 1)
+        if m == 0:
+            assert not out[b].any()
+            continue
+        want, A, Bs = attend64(f64(q[b]), rows[b % 3, :, :m].cpu().numpy())
+        check(out[b], want, A, Bs, m, dtype)
+
+
+def test_a_length_past_the_block_table_is_reported(sk):
+    """More tokens than the table has entries for: the error word says so, and every read
+    stays inside the pool."""
+    P = sk.PagedLayer.allocate(2, 2, 64, block_size=16, n_blocks=8, max_blocks=3, sinks=2, window=20, bits=4)
+    P.block_table.copy_(torch.arange(6).view(2, 3))
+    P.k_pool.copy_(rows_of((8, 2, 16), 64, 77))
+    P.seq_lens.copy_(torch.tensor([1 << 60, 30]))
+    q = randn((2, 4, 64), 78, BF)
+    out = sk.paged_decode_attention(P, q)
+    assert P.error_bits() == sk.SK_DEVERR_BLOCK_TABLE
+    P.err.zero_()
+    P.seq_lens.copy_(torch.tensor([48, 30]))
+    again = sk.paged_decode_attention(P, q)
+    assert torch.equal(out[1], again[1]) and P.error_bits() == 0
+
+
+def test_rerotation_and_shift_refuse_4_bit_layers(sk):
+    a = sk.KVLayer.allocate(sk.SK_LAYER_RING, 1, 2, 64, sinks=1, window=7, bits=4)
+    t = [sk.RopeTable(64, 64, 1e4, 64, yarn_factor=f, yarn_orig_ctx=8) for f in (1.0, 2.0)]
+    for call in (lambda: sk.kv_rerotate([a], t[0], t[1]), lambda: sk.kv_shift_recent([a], t[0], -1)):
+        with pytest.raises(sk.SinkKVError) as e:
+            call()
+        assert e.value.status == sk.SK_ERR_UNSUPPORTED
+
+
 def test_noalloc_and_given_buffers(sk):
     D, n, Hq, Hkv = 128, 300, 8, 2
     a = sk.KVLayer.allocate(sk.SK_LAYER_GLOBAL, 2, Hkv, D, capacity=n, bits=4)
