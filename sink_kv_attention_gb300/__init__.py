@@ -414,15 +414,13 @@ class KVLayer:
         return _row_head_dim(self.k)
 
     def struct(self) -> KVLayerStruct:
-        _need_contig(self.k, self.v, self.k_scale, self.head, self.count, self.pos)
-        kd = _sk_dtype(self.k.dtype)
-        return KVLayerStruct(self.kind, kd, kd if self.v is None else _sk_dtype(self.v.dtype), self.batch,
-                             self.n_kv_heads, self.head_dim, self.sinks, self.window, self.capacity,
-                             self.k.data_ptr(), None if self.v is None else self.v.data_ptr(),
-                             None if self.k_scale is None else self.k_scale.data_ptr(),
-                             None if self.head is None else self.head.data_ptr(),
-                             None if self.count is None else self.count.data_ptr(),
-                             self.pos.data_ptr(), None if self.err is None else self.err.data_ptr())
+        k, v = self.k, self.v
+        _need_contig(k, v, self.k_scale, self.head, self.count, self.pos)
+        kd = _sk_dtype(k.dtype)
+        B, H, cap, _ = k.shape
+        return KVLayerStruct(self.kind, kd, kd if v is None else _sk_dtype(v.dtype), B, H, _row_head_dim(k),
+                             self.sinks, self.window, cap, k.data_ptr(), _ptr(v), _ptr(self.k_scale),
+                             _ptr(self.head), _ptr(self.count), self.pos.data_ptr(), _ptr(self.err))
 
     def error_bits(self) -> int:
         """Read the device error word (synchronises)."""

@@ -12,7 +12,8 @@
 // decisions are integers over a few hundred KB, bound by the latency of a handful of
 // dependent steps, so each call's bookkeeping is one launch of one cluster of 8 blocks whose
 // barriers separate the steps (a grid-wide barrier in hardware; a launch per step took
-// 2-3 us each); a second launch moves pages at the rate of the memory.
+// 2-3 us each); pages are moved by a second launch, at the rate of the memory, unless they are
+// few.
 #include <algorithm>
 
 #include "common.cuh"
@@ -81,6 +82,70 @@ __device__ __forceinline__ int before_warp(int x, int warp_of_all, int* s, int* 
 }
 
 // ---------------------------------------------------------------------------
+// Moving pages
+// ---------------------------------------------------------------------------
+
+struct MoveParams {
+    void* pool[2 * kMaxLayers];
+    int32_t bytes[2 * kMaxLayers];  // of a page of the pool
+    int n_pools;
+    const int32_t* src;  // move i: block src[i * stride] to dst[i * stride]; none where src < 0
+    const int32_t* dst;
+    const int32_t* n;    // moves, on the device, or null: n_most
+    int n_most, stride;
+    // compact: the tables to rewrite, or null
+    const int32_t* map;
+    int32_t* table;
+    int64_t entries, NB;
+};
+
+constexpr int kMoveThreads = 256;
+constexpr int kMoveUnroll = 8;
+constexpr int kPiece = 32 * 16 * kMoveUnroll;  // bytes a warp moves at a time
+
+// Warp `warp` of `warps` takes its pieces of 4 KB of the n moves, 8 loads of 16 bytes a lane in
+// flight.  The moves' blocks are all different: sources are in use, destinations were free.
+__device__ __forceinline__ void move_pieces(const MoveParams& p, int n, int64_t warp, int64_t warps, int lane) {
+    for (int l = 0; l < p.n_pools; ++l) {
+        const int bytes = p.bytes[l];
+        const int pieces = (bytes + kPiece - 1) / kPiece;
+        const int64_t total = int64_t(n) * pieces;
+        for (int64_t i = warp; i < total; i += warps) {
+            const int m = int(i / pieces), at = int(i % pieces) * kPiece + lane * 16;
+            const int64_t from = __ldcg(p.src + int64_t(m) * p.stride);
+            if (from < 0) continue;
+            const uint8_t* a = static_cast<const uint8_t*>(p.pool[l]) + from * bytes + at;
+            uint8_t* b = static_cast<uint8_t*>(p.pool[l]) + int64_t(__ldcg(p.dst + int64_t(m) * p.stride)) * bytes + at;
+            uint4 v[kMoveUnroll];
+#pragma unroll
+            for (int u = 0; u < kMoveUnroll; ++u)
+                if (at + u * 512 < bytes) v[u] = __ldcs(reinterpret_cast<const uint4*>(a + u * 512));
+#pragma unroll
+            for (int u = 0; u < kMoveUnroll; ++u)
+                if (at + u * 512 < bytes) __stcs(reinterpret_cast<uint4*>(b + u * 512), v[u]);
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kMoveThreads) move_pages_kernel(const __grid_constant__ MoveParams p) {
+    pdl_trigger();
+    pdl_wait();
+    if (p.map != nullptr) {
+        for (int64_t i = int64_t(blockIdx.x) * kMoveThreads + threadIdx.x; i < p.entries;
+             i += int64_t(gridDim.x) * kMoveThreads) {
+            const int32_t e = p.table[i];
+            if (e >= 0 && e < p.NB) {
+                const int32_t to = p.map[e];
+                if (to != e) p.table[i] = to;
+            }
+        }
+    }
+    move_pieces(p, p.n != nullptr ? *p.n : p.n_most,
+                int64_t(blockIdx.x) * (kMoveThreads / 32) + (threadIdx.x >> 5),
+                int64_t(gridDim.x) * (kMoveThreads / 32), threadIdx.x & 31);
+}
+
+// ---------------------------------------------------------------------------
 // reserve
 // ---------------------------------------------------------------------------
 
@@ -143,7 +208,10 @@ __device__ __forceinline__ void load_entries(const ReserveParams& p, const int32
     for (int u = 0; u < kAhead; ++u) shared[u] = r[u] > 1;
 }
 
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1) reserve_kernel(ReserveParams p) {
+// `moves`: the copies to make here, where they are few bytes at most; n_pools = 0 leaves them
+// to move_pages_kernel.
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
+    reserve_kernel(ReserveParams p, const __grid_constant__ MoveParams moves) {
     __shared__ int s_scan[kAllWarps + kWarps];
     __shared__ int s_shared[kMaxBatch];            // shared_of, in every block
     __shared__ int s_base[kMaxBatch];              // rank of a request's first new block, or -1: not granted
@@ -331,69 +399,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1) 
         const int32_t e = __ldcg(p.old_ids + r);
         if (e >= 0) atomicSub(p.ref + e, 1);
     }
-}
-
-// ---------------------------------------------------------------------------
-// Moving pages
-// ---------------------------------------------------------------------------
-
-struct MoveParams {
-    void* pool[2 * kMaxLayers];
-    int32_t bytes[2 * kMaxLayers];  // of a page of the pool
-    int n_pools;
-    const int32_t* src;  // move i: block src[i * stride] to dst[i * stride]; none where src < 0
-    const int32_t* dst;
-    const int32_t* n;    // moves, on the device, or null: n_most
-    int n_most, stride;
-    // compact: the tables to rewrite, or null
-    const int32_t* map;
-    int32_t* table;
-    int64_t entries, NB;
-};
-
-constexpr int kMoveThreads = 256;
-constexpr int kMoveUnroll = 8;
-constexpr int kPiece = 32 * 16 * kMoveUnroll;  // bytes a warp moves at a time
-
-// The moves' blocks are all different: sources are in use, destinations were free.  A warp
-// moves a piece of 4 KB of a page, 8 loads of 16 bytes a lane in flight.
-__global__ void __launch_bounds__(kMoveThreads) move_pages_kernel(const __grid_constant__ MoveParams p) {
-    pdl_trigger();
-    pdl_wait();
-    if (p.map != nullptr) {
-        for (int64_t i = int64_t(blockIdx.x) * kMoveThreads + threadIdx.x; i < p.entries;
-             i += int64_t(gridDim.x) * kMoveThreads) {
-            const int32_t e = p.table[i];
-            if (e >= 0 && e < p.NB) {
-                const int32_t to = p.map[e];
-                if (to != e) p.table[i] = to;
-            }
-        }
-    }
-    const int n = p.n != nullptr ? *p.n : p.n_most;
-    const int lane = threadIdx.x & 31;
-    const int64_t warps = int64_t(gridDim.x) * (kMoveThreads / 32);
-    const int64_t warp = int64_t(blockIdx.x) * (kMoveThreads / 32) + (threadIdx.x >> 5);
-    if (n == 0) return;
-    for (int l = 0; l < p.n_pools; ++l) {
-        const int bytes = p.bytes[l];
-        const int pieces = (bytes + kPiece - 1) / kPiece;
-        const int64_t total = int64_t(n) * pieces;
-        for (int64_t i = warp; i < total; i += warps) {
-            const int m = int(i / pieces), at = int(i % pieces) * kPiece + lane * 16;
-            const int64_t from = p.src[int64_t(m) * p.stride];
-            if (from < 0) continue;
-            const uint8_t* a = static_cast<const uint8_t*>(p.pool[l]) + from * bytes + at;
-            uint8_t* b = static_cast<uint8_t*>(p.pool[l]) + int64_t(p.dst[int64_t(m) * p.stride]) * bytes + at;
-            uint4 v[kMoveUnroll];
-#pragma unroll
-            for (int u = 0; u < kMoveUnroll; ++u)
-                if (at + u * 512 < bytes) v[u] = __ldcs(reinterpret_cast<const uint4*>(a + u * 512));
-#pragma unroll
-            for (int u = 0; u < kMoveUnroll; ++u)
-                if (at + u * 512 < bytes) __stcs(reinterpret_cast<uint4*>(b + u * 512), v[u]);
-        }
-    }
+    move_pieces(moves, moves.n_most, wa, kAllWarps, lane);
 }
 
 // ---------------------------------------------------------------------------
@@ -619,6 +625,10 @@ void move_pools(const sk_paged_layer* layers, int n_layers, MoveParams* m) {
             }
 }
 
+// Copies of at most this many bytes are made by the reserving cluster itself, at the rate of its
+// 8 SMs: a second launch costs the host about 5 us and the device 3 to 5 us.
+constexpr int64_t kCopyHere = 2 << 20;
+
 // One block per piece of the most that can move, at most 8 per SM.
 unsigned move_grid(const MoveParams& m, int64_t pages) {
     const int64_t pieces = pages * ((m.bytes[0] + kPiece - 1) / kPiece);
@@ -668,13 +678,18 @@ extern "C" sk_status sk_paged_reserve(const sk_paged_layer* layers, int32_t n_la
     p.free_ids = ws + ws_ids(L);
     p.old_ids = p.free_ids + L.n_blocks;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    SK_CUDA_RET(launch_pdl(reserve_kernel, dim3(kCluster), dim3(kThreads), 0, st, p));
     MoveParams m{};
     move_pools(layers, n_layers, &m);
     m.src = p.copies;
     m.dst = p.copies + 1;
     m.stride = 2;
     m.n_most = L.batch;
+    int64_t most = 0;  // bytes, if every request copies a block
+    for (int i = 0; i < m.n_pools; ++i) most += int64_t(L.batch) * m.bytes[i];
+    MoveParams here{};
+    if (most <= kCopyHere) here = m;
+    SK_CUDA_RET(launch_pdl(reserve_kernel, dim3(kCluster), dim3(kThreads), 0, st, p, here));
+    if (most <= kCopyHere) return SK_OK;
     SK_CUDA_RET(launch_pdl(move_pages_kernel, dim3(move_grid(m, L.batch)), dim3(kMoveThreads), 0, st, m));
     return SK_OK;
 }
