@@ -89,10 +89,11 @@ struct MoveParams {
     void* pool[2 * kMaxLayers];
     int32_t bytes[2 * kMaxLayers];  // of a page of the pool
     int n_pools;
-    const int32_t* src;  // move i: block src[i * stride] to dst[i * stride]; none where src < 0
+    int pieces;          // of kPiece bytes in the largest page
+    const int32_t* src;  // move i: block src[i * stride] to dst[i * stride]
     const int32_t* dst;
-    const int32_t* n;    // moves, on the device, or null: n_most
-    int n_most, stride;
+    const int32_t* n;    // moves, on the device
+    int stride;
     // compact: the tables to rewrite, or null
     const int32_t* map;
     int32_t* table;
@@ -103,27 +104,48 @@ constexpr int kMoveThreads = 256;
 constexpr int kMoveUnroll = 8;
 constexpr int kPiece = 32 * 16 * kMoveUnroll;  // bytes a warp moves at a time
 
-// Warp `warp` of `warps` takes its pieces of 4 KB of the n moves, 8 loads of 16 bytes a lane in
-// flight.  The moves' blocks are all different: sources are in use, destinations were free.
-__device__ __forceinline__ void move_pieces(const MoveParams& p, int n, int64_t warp, int64_t warps, int lane) {
-    for (int l = 0; l < p.n_pools; ++l) {
+// Warp `warp` of `warps` takes every warps-th piece of 4 KB of the n moves in all pools, 8 loads
+// of 16 bytes a lane in flight; the ids of its next piece are on their way meanwhile.  (Pools one
+// after the other, each with its ids to wait for, took 0.4 us a pool.)  Pieces are counted as if
+// every page were the largest.  The moves' blocks are all different: sources are in use,
+// destinations were free.
+__device__ __forceinline__ void move_pieces(const MoveParams& p, uint32_t n, uint32_t warp, uint32_t warps, int lane) {
+    const uint32_t pieces = uint32_t(p.pieces), pools = uint32_t(p.n_pools);
+    if (n == 0 || pools == 0) return;
+    const uint32_t step_m = warps / pieces, step_pc = warps % pieces;
+    uint32_t m = warp / pieces, pc = warp % pieces, l = m / n;
+    m %= n;
+    if (l >= pools) return;
+    int32_t from = __ldcg(p.src + int64_t(m) * p.stride), to = __ldcg(p.dst + int64_t(m) * p.stride);
+    for (;;) {
         const int bytes = p.bytes[l];
-        const int pieces = (bytes + kPiece - 1) / kPiece;
-        const int64_t total = int64_t(n) * pieces;
-        for (int64_t i = warp; i < total; i += warps) {
-            const int m = int(i / pieces), at = int(i % pieces) * kPiece + lane * 16;
-            const int64_t from = __ldcg(p.src + int64_t(m) * p.stride);
-            if (from < 0) continue;
-            const uint8_t* a = static_cast<const uint8_t*>(p.pool[l]) + from * bytes + at;
-            uint8_t* b = static_cast<uint8_t*>(p.pool[l]) + int64_t(__ldcg(p.dst + int64_t(m) * p.stride)) * bytes + at;
-            uint4 v[kMoveUnroll];
+        const int64_t at = int64_t(pc) * kPiece + lane * 16;
+        uint8_t* const pool = static_cast<uint8_t*>(p.pool[l]);
+        const uint8_t* a = pool + int64_t(from) * bytes + at;
+        uint8_t* b = pool + int64_t(to) * bytes + at;
+        uint4 v[kMoveUnroll];
 #pragma unroll
-            for (int u = 0; u < kMoveUnroll; ++u)
-                if (at + u * 512 < bytes) v[u] = __ldcs(reinterpret_cast<const uint4*>(a + u * 512));
-#pragma unroll
-            for (int u = 0; u < kMoveUnroll; ++u)
-                if (at + u * 512 < bytes) __stcs(reinterpret_cast<uint4*>(b + u * 512), v[u]);
+        for (int u = 0; u < kMoveUnroll; ++u)
+            if (at + u * 512 < bytes) v[u] = __ldcs(reinterpret_cast<const uint4*>(a + u * 512));
+        pc += step_pc;
+        m += step_m;
+        if (pc >= pieces) {
+            pc -= pieces;
+            ++m;
         }
+        if (m >= n) {
+            l += m / n;
+            m %= n;
+        }
+        const bool more = l < pools;
+        if (more) {
+            from = __ldcg(p.src + int64_t(m) * p.stride);
+            to = __ldcg(p.dst + int64_t(m) * p.stride);
+        }
+#pragma unroll
+        for (int u = 0; u < kMoveUnroll; ++u)
+            if (at + u * 512 < bytes) __stcs(reinterpret_cast<uint4*>(b + u * 512), v[u]);
+        if (!more) return;
     }
 }
 
@@ -140,9 +162,8 @@ __global__ void __launch_bounds__(kMoveThreads) move_pages_kernel(const __grid_c
             }
         }
     }
-    move_pieces(p, p.n != nullptr ? *p.n : p.n_most,
-                int64_t(blockIdx.x) * (kMoveThreads / 32) + (threadIdx.x >> 5),
-                int64_t(gridDim.x) * (kMoveThreads / 32), threadIdx.x & 31);
+    move_pieces(p, uint32_t(*p.n), blockIdx.x * (kMoveThreads / 32) + (threadIdx.x >> 5),
+                gridDim.x * (kMoveThreads / 32), threadIdx.x & 31);
 }
 
 // ---------------------------------------------------------------------------
@@ -163,7 +184,8 @@ struct ReserveParams {
     int32_t* old_ids;      // [NB] the shared block that free_ids[i] takes the place of, or -1
     int32_t* need;         // [B] blocks wanted; kRefused, kNothing
     int32_t* shared_of;    // [B] the shared block in which the request's next token falls, or -1
-    int32_t* copies;       // [B][2] block to copy and its copy, or -1
+    int32_t* copies;       // [n_copies][2] a block to copy and its copy
+    int32_t* n_copies;
     int32_t* counts;       // [kAllWarps]
 };
 
@@ -224,6 +246,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
     pdl_trigger();
     pdl_wait();
 
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.n_copies = 0;
     if (threadIdx.x < p.B) {
         s_len[threadIdx.x] = p.lens[threadIdx.x];
         s_new[threadIdx.x] = p.n_new != nullptr ? p.n_new[threadIdx.x] : 1;
@@ -388,9 +411,10 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
         }
         src = __shfl_sync(kFull, src, 0);
         dst = __shfl_sync(kFull, dst, 0);
-        if (lane == 0) {
-            p.copies[2 * b2] = src;
-            p.copies[2 * b2 + 1] = dst;
+        if (lane == 0 && src >= 0) {  // their order decides only which warp copies which
+            const int i = atomicAdd(p.n_copies, 1);
+            p.copies[2 * i] = src;
+            p.copies[2 * i + 1] = dst;
         }
     }
     if (!any_shared) return;
@@ -399,7 +423,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
         const int32_t e = __ldcg(p.old_ids + r);
         if (e >= 0) atomicSub(p.ref + e, 1);
     }
-    move_pieces(moves, moves.n_most, wa, kAllWarps, lane);
+    if (moves.n_pools > 0) move_pieces(moves, uint32_t(__ldcg(moves.n)), wa, kAllWarps, lane);
 }
 
 // ---------------------------------------------------------------------------
@@ -622,16 +646,20 @@ void move_pools(const sk_paged_layer* layers, int n_layers, MoveParams* m) {
             if (const size_t bytes = page_bytes(layers[i], v != 0)) {
                 m->pool[m->n_pools] = v ? layers[i].v_pool : layers[i].k_pool;
                 m->bytes[m->n_pools++] = int32_t(bytes);
+                m->pieces = std::max(m->pieces, int((bytes + kPiece - 1) / kPiece));
             }
 }
 
-// Copies of at most this many bytes are made by the reserving cluster itself, at the rate of its
-// 8 SMs: a second launch costs the host about 5 us and the device 3 to 5 us.
+// Where all requests together could copy at most this many bytes, the reserving cluster makes the
+// copies itself, at the rate of its 8 SMs.  Most calls of a serving loop copy nothing, and a second
+// launch costs those 0.5-1 us on the device and 1-1.5 us of the host's time at any size.  When
+// every request copies, the cluster takes (against two launches, on the device) 7.6 us (8.2) for
+// 20 KB, 8.7 (8.4) for 80 KB, 10.9 (9.9) for 320 KB, 13.7 (10.3) for 2 MB and 17.3 (9.3) for 4 MB.
 constexpr int64_t kCopyHere = 2 << 20;
 
 // One block per piece of the most that can move, at most 8 per SM.
 unsigned move_grid(const MoveParams& m, int64_t pages) {
-    const int64_t pieces = pages * ((m.bytes[0] + kPiece - 1) / kPiece);
+    const int64_t pieces = pages * m.pieces * m.n_pools;
     return unsigned(std::max<int64_t>(1, std::min<int64_t>((pieces + kMoveThreads / 32 - 1) / (kMoveThreads / 32),
                                                            int64_t(device_sm_count()) * 8)));
 }
@@ -672,6 +700,7 @@ extern "C" sk_status sk_paged_reserve(const sk_paged_layer* layers, int32_t n_la
     p.W = L.window;
     p.sink_len = L.n_sink_blocks * L.block_size;
     p.counts = ws;
+    p.n_copies = ws + kWsScalars + 2;
     p.need = ws + kWsRequests;
     p.shared_of = p.need + L.batch;
     p.copies = p.shared_of + L.batch;
@@ -683,7 +712,7 @@ extern "C" sk_status sk_paged_reserve(const sk_paged_layer* layers, int32_t n_la
     m.src = p.copies;
     m.dst = p.copies + 1;
     m.stride = 2;
-    m.n_most = L.batch;
+    m.n = p.n_copies;
     int64_t most = 0;  // bytes, if every request copies a block
     for (int i = 0; i < m.n_pools; ++i) most += int64_t(L.batch) * m.bytes[i];
     MoveParams here{};

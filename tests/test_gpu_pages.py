@@ -185,6 +185,30 @@ def test_compact(sk, B, MB, NB, nsb, share, kinds):
     assert layers[0].error_bits() == 0
 
 
+@pytest.mark.parametrize("B,n_layers", [(4, 3), (6, 41), (200, 31), (2, 128)])
+def test_copies_and_moves_in_many_layers_of_unequal_pages(sk, B, n_layers):
+    """A reserve that copies half of the requests' last pages, then a compaction, in pools whose
+    pages differ in size (pieces of a page that a smaller one has not are not moved)."""
+    rng = np.random.default_rng(B + n_layers)
+    kinds = [("i4", "bf16", "f32")[int(rng.integers(0, 3))] for _ in range(n_layers)]
+    layers, group, table, ref, lens, sink_ids = build(sk, rng, B, 5, 6 * B + 8, 32, kinds=kinds, share=2, fill=0.9)
+    pools = pools_of(layers)
+    granted = group.reserve()
+    want, copies = pages_reserve(table, ref, lens.tolist(), [1] * B, 32, 0, 0, 0)
+    for src, dst in copies:
+        for p in pools:
+            p[dst] = p[src]
+    assert granted.tolist() == want
+    check_state(layers, group, table, ref, pools)
+    block_map, used = group.compact()
+    want_map, want_used, moves = pages_compact(table, ref, sink_ids)
+    for src, dst in moves:
+        for p in pools:
+            p[dst] = p[src]
+    assert np.array_equal(block_map.cpu().numpy(), want_map) and used.item() == want_used
+    check_state(layers, group, table, ref, pools)
+
+
 def test_compact_of_an_empty_pool(sk):
     P = sk.PagedLayer.allocate(2, 2, 64, block_size=8, n_blocks=100, max_blocks=3)
     block_map, used = sk.PagedGroup([P]).compact()
