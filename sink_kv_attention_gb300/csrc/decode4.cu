@@ -56,6 +56,10 @@
 // Rows are visited in an order that spreads a quarter warp's 16-byte loads over all
 // banks: matrix row r of a 16-row tile is key kappa(r), chosen so that (0,1), (2,3), ..
 // are 16 words apart mod 32 (K fragments) and so are (0,2,4,6) and (1,3,5,7) 8 apart (V).
+//
+// The code around the tile loop runs once or twice in a launch and is fetched once, so its
+// loops are not unrolled (a kernel of 126 KB became one of 77 KB: calls of 5 to 25 us 1-5%
+// faster, code warm).
 #include "decode4.cuh"
 
 #include <atomic>
@@ -429,22 +433,32 @@ __device__ __noinline__ void combine_unit(const DecodeParams& p, int64_t unit, c
     fetch(0);
     float* ls = w + n * HEADS;        // [n][HEADS] sums of weights
     float* top = ls + n * HEADS;      // [HEADS] reference, then the sum of weights
-    for (int i = threadIdx.x; i < n * HEADS; i += THREADS) {
-        const float* ml = first + int64_t(i / HEADS) * PF + HEADS * D + i % HEADS;
-        w[i] = __ldcg(ml);
-        ls[i] = __ldcg(ml + HEADS);
-    }
-    __syncthreads();
-    if (threadIdx.x < HEADS) {
+    const int lane = threadIdx.x & 31;
+    // a warp per head, a lane per partial (a thread per head took 0.3 us longer at 4 partials)
+    for (int k = threadIdx.x >> 5; k < HEADS; k += THREADS / 32) {
         float M = -INFINITY, l = 0.0f;
-        for (int i = 0; i < n; ++i) M = fmaxf(M, w[i * HEADS + threadIdx.x]);
-        for (int i = 0; i < n; ++i) {
-            const float f = fast_exp2_approx(w[i * HEADS + threadIdx.x] - M);
-            w[i * HEADS + threadIdx.x] = f;
-            l = fmaf(ls[i * HEADS + threadIdx.x], f, l);
+#pragma unroll 2
+        for (int i = lane; i < n; i += 32) {
+            const float* ml = first + int64_t(i) * PF + HEADS * D + k;
+            const float m = __ldcg(ml);
+            w[i * HEADS + k] = m;
+            ls[i * HEADS + k] = __ldcg(ml + HEADS);
+            M = fmaxf(M, m);
         }
-        top[threadIdx.x] = M;
-        top[HEADS + threadIdx.x] = l;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+#pragma unroll 1
+        for (int i = lane; i < n; i += 32) {
+            const float f = fast_exp2_approx(w[i * HEADS + k] - M);
+            w[i * HEADS + k] = f;
+            l = fmaf(ls[i * HEADS + k], f, l);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(kFull, l, o);
+        if (lane == 0) {
+            top[k] = M;
+            top[HEADS + k] = l;
+        }
     }
     __syncthreads();
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -476,6 +490,7 @@ __device__ __forceinline__ bool mark_partial(uint64_t* marks, int own, int n, ui
     __syncwarp();
     __threadfence();
     bool all = true;
+#pragma unroll 1
     for (int i = lane; i < n; i += 32) all = all && m[i] == tag;
     return __all_sync(kFull, all);
 }
@@ -525,6 +540,7 @@ __global__ void __launch_bounds__(Cfg4<T, D, NREP, KVH>::THREADS, 1) decode4_ker
     for (int pass = 0; pass < 2; ++pass) {
         if (pass == 1) pdl_wait();  // the append has written the state, q and the new rows
         bool changed = false;
+#pragma unroll 1
         for (int b = threadIdx.x; b < p.B; b += C::THREADS) {
             int64_t n, shift = 0;
             if constexpr (PAGED) {
@@ -552,6 +568,7 @@ __global__ void __launch_bounds__(Cfg4<T, D, NREP, KVH>::THREADS, 1) decode4_ker
         if (!__syncthreads_or(changed)) break;
         if (warp == 0) {  // rows before each sequence, uncounted extras left out for now
             int64_t carry = 0;
+#pragma unroll 1
             for (int b0 = 0; b0 < p.B; b0 += 32) {
                 const int b = b0 + lane;
                 int64_t x = b < p.B ? p.Hkv * rows.len[b] : 0;
@@ -587,6 +604,7 @@ __global__ void __launch_bounds__(Cfg4<T, D, NREP, KVH>::THREADS, 1) decode4_ker
         __syncthreads();  // every thread has R
         if (warp == 0) {
             int before = 0;  // sequences with rows
+#pragma unroll 1
             for (int b0 = 0; b0 < p.B; b0 += 32) {
                 const int b = b0 + lane;
                 const uint32_t m = __ballot_sync(kFull, b < p.B && rows.len[b] > 0);
@@ -604,8 +622,10 @@ __global__ void __launch_bounds__(Cfg4<T, D, NREP, KVH>::THREADS, 1) decode4_ker
     }
 
     // sequences with nothing visible: zeros, each from one block
+#pragma unroll 1
     for (int b = blockIdx.x; b < p.B; b += gridDim.x)
         if (rows.len[b] == 0)
+#pragma unroll 1
             for (int i = threadIdx.x; i < p.Hkv * HEADS * D; i += C::THREADS)
                 static_cast<T*>(p.out)[int64_t(b) * p.Hkv * HEADS * D + i] = T(0.0f);
     if (c >= P) return;  // R = 0 too
@@ -745,6 +765,7 @@ __global__ void __launch_bounds__(Cfg4<T, D, NREP, KVH>::THREADS, 1) decode4_ker
             if (n < TR) {  // rows past the tile's last one: zeros (whatever the slot held)
 #pragma unroll
                 for (int kv = 0; kv < KVH; ++kv)
+#pragma unroll 1
                     for (int i = n * C::ROWB + lane * 16; i < C::HEAD_BYTES; i += 512)
                         *reinterpret_cast<uint4*>(tile + kv * C::HEAD_BYTES + i) = make_uint4(0, 0, 0, 0);
                 __syncwarp();
@@ -983,6 +1004,7 @@ __global__ void __launch_bounds__(Cfg4<T, D, NREP, KVH>::THREADS, 1) decode4_ker
         __syncthreads();
         const bool whole = w.u.rows == rows.len[w.u.b];
         float* part = partials + (unit + c) * C::PARTIAL_FLOATS;
+#pragma unroll 1
         for (int idx = threadIdx.x; idx < HEADS * D / 4; idx += C::THREADS) {
             const int h = idx / (D / 4);
             const float4* ms = reinterpret_cast<const float4*>(warp_m + h * NWARPS);
@@ -1056,6 +1078,7 @@ __global__ void __launch_bounds__(Cfg4<T, D, NREP, KVH>::THREADS, 1) decode4_ker
             if (!warp_slot[i]) continue;
             combine_unit<T, D, HEADS, C::PARTIAL_FLOATS, C::THREADS>(
                 p, cut.unit, partials + cut.first * C::PARTIAL_FLOATS, cut.n, reinterpret_cast<float*>(smem));
+#pragma unroll 1
             for (int j = threadIdx.x; j < cut.n; j += C::THREADS) marks[cut.first + j] = 0;
         }
     }
