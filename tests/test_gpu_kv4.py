@@ -567,6 +567,33 @@ def test_units_cut_between_blocks_in_graphs_that_share_a_workspace(sk):
             assert torch.equal(sk.decode_attention(layers[1], qs[1], workspace=ws), want[1])
 
 
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+def test_two_calls_at_once(sk, dtype):
+    """Calls of two streams that share the GPU, each with its own workspace, over units cut
+    between blocks: always the bits of the call alone."""
+    D, rep, cases = 128, 4, [(2, 2, 9001), (5, 4, 1500)]
+    layers, qs, wss, want = [], [], [], []
+    for i, (B, Hkv, n) in enumerate(cases):
+        a = sk.KVLayer.allocate(sk.SK_LAYER_GLOBAL, B, Hkv, D, capacity=n, bits=4)
+        a.k.copy_(rows_of((B, Hkv, n), D, 300 + i))
+        a.pos.copy_(torch.tensor([n, n // 3, 0, 1, n - 1][:B]))
+        layers.append(a)
+        qs.append(randn((B, Hkv * rep, D), 310 + i, dtype))
+        wss.append(torch.empty(sk.decode_workspace_bytes(a, Hkv * rep), dtype=torch.uint8, device="cuda"))
+        want.append(sk.decode_attention(a, qs[i], workspace=wss[i]).clone())
+    rounds = 40
+    outs = [torch.zeros((rounds,) + tuple(q.shape), dtype=dtype, device="cuda") for q in qs]
+    streams = [torch.cuda.Stream() for _ in cases]
+    for st in streams:
+        st.wait_stream(torch.cuda.current_stream())
+    for r in range(rounds):
+        for i, st in enumerate(streams):
+            sk.decode_attention(layers[i], qs[i], out=outs[i][r], workspace=wss[i], stream=st)
+    torch.cuda.synchronize()
+    for i in range(len(cases)):
+        assert all(torch.equal(outs[i][r], want[i]) for r in range(rounds))
+
+
 @pytest.mark.parametrize("kind", ["ring", "global"])
 def test_prefill_over_a_4_bit_prior(sk, kind):
     """A chunk over a 4-bit prior gives the bits of the same chunk over a bf16 cache that
