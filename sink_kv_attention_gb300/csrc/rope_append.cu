@@ -219,7 +219,7 @@ template <> struct CacheStore<__nv_bfloat16> {
 // per 8 dims: by each lane for bf16 rows, by the even lane of a pair for fp32 rows.
 //
 // What bounds the 4-bit append: a prompt's chunk of 32,768 tokens (32 and 8 heads, d_h 128)
-// takes 140 us for 640 MB, with 69% of the issue slots and 62% of the integer pipe used, DRAM
+// takes 140 us for 797 MB, with 69% of the issue slots and 62% of the integer pipe used, DRAM
 // at 65%.  Measured and left out: three blocks an SM (170 us), the next row's load ahead (149),
 // two rows at a time (142).
 template <typename IO, int D>
