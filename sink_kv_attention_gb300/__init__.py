@@ -190,16 +190,15 @@ def _stream(stream) -> int:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
+_SK_DTYPES = {torch.bfloat16: SK_BF16, torch.float32: SK_F32, torch.int8: SK_I8,
+              torch.uint8: SK_I4}  # uint8: rows of 4-bit codes and their parameters
+
+
 def _sk_dtype(dt: torch.dtype) -> int:
-    if dt == torch.bfloat16:
-        return SK_BF16
-    if dt == torch.float32:
-        return SK_F32
-    if dt == torch.int8:
-        return SK_I8
-    if dt == torch.uint8:
-        return SK_I4  # rows of 4-bit codes and their parameters
-    raise TypeError(f"unsupported dtype {dt}")
+    d = _SK_DTYPES.get(dt)
+    if d is None:
+        raise TypeError(f"unsupported dtype {dt}")
+    return d
 
 
 def kv4_row_bytes(head_dim: int) -> int:
@@ -207,13 +206,15 @@ def kv4_row_bytes(head_dim: int) -> int:
     return head_dim + head_dim // 4
 
 
+def _kv4_head_dim(row_bytes: int) -> int:
+    if row_bytes % 5:
+        raise ValueError("rows are not 4-bit cache rows")
+    return row_bytes // 5 * 4
+
+
 def _row_head_dim(k: torch.Tensor) -> int:
     """head_dim of a cache buffer [..., row]: its last size, or that of 4-bit rows."""
-    if k.dtype != torch.uint8:
-        return k.shape[-1]
-    if k.shape[-1] % 5:
-        raise ValueError("rows are not 4-bit cache rows")
-    return k.shape[-1] // 5 * 4
+    return _kv4_head_dim(k.shape[-1]) if k.dtype == torch.uint8 else k.shape[-1]
 
 
 def _need_contig(*ts):
@@ -414,13 +415,16 @@ class KVLayer:
         return _row_head_dim(self.k)
 
     def struct(self) -> KVLayerStruct:
-        k, v = self.k, self.v
-        _need_contig(k, v, self.k_scale, self.head, self.count, self.pos)
+        k, v, ks, head, count, pos, err = (self.k, self.v, self.k_scale, self.head, self.count, self.pos,
+                                           self.err)
+        _need_contig(k, v, ks, head, count, pos)
         kd = _sk_dtype(k.dtype)
-        B, H, cap, _ = k.shape
-        return KVLayerStruct(self.kind, kd, kd if v is None else _sk_dtype(v.dtype), B, H, _row_head_dim(k),
-                             self.sinks, self.window, cap, k.data_ptr(), _ptr(v), _ptr(self.k_scale),
-                             _ptr(self.head), _ptr(self.count), self.pos.data_ptr(), _ptr(self.err))
+        B, H, cap, D = k.shape
+        return KVLayerStruct(self.kind, kd, kd if v is None else _sk_dtype(v.dtype), B, H,
+                             _kv4_head_dim(D) if kd == SK_I4 else D, self.sinks, self.window, cap, k.data_ptr(),
+                             None if v is None else v.data_ptr(), None if ks is None else ks.data_ptr(),
+                             None if head is None else head.data_ptr(), None if count is None else count.data_ptr(),
+                             pos.data_ptr(), None if err is None else err.data_ptr())
 
     def error_bits(self) -> int:
         """Read the device error word (synchronises)."""
@@ -479,16 +483,17 @@ def decode_attention(layer: KVLayer, q_rot: torch.Tensor, out: Optional[torch.Te
     Hq = q_rot.shape[1]
     if out is None:
         out = torch.empty_like(q_rot)
-    s = layer.struct()
-    need = int(_lib().sk_decode_workspace_bytes(ctypes.byref(s), Hq))
+    lib, s = _lib(), layer.struct()
+    ref = ctypes.byref(s)
+    need = lib.sk_decode_workspace_bytes(ref, Hq)
     if need == 0:
         raise SinkKVError(SK_ERR_UNSUPPORTED, "sk_decode_workspace_bytes")
-    if workspace is None or workspace.numel() * workspace.element_size() < need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q_rot.device)
-    _check(_lib().sk_decode_attention(ctypes.byref(s), _ptr(q_rot), Hq, _sk_dtype(q_rot.dtype),
-                                      _sink_logits(sink_logits, Hq), _ptr(out), _ptr(workspace),
-                                      workspace.numel() * workspace.element_size(), _stream(stream)),
-           "sk_decode_attention")
+    size = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    if size < need:
+        size, workspace = need, torch.empty(need, dtype=torch.uint8, device=q_rot.device)
+    _check(lib.sk_decode_attention(ref, q_rot.data_ptr(), Hq, _sk_dtype(q_rot.dtype),
+                                   _sink_logits(sink_logits, Hq), out.data_ptr(), workspace.data_ptr(), size,
+                                   _stream(stream)), "sk_decode_attention")
     return out
 
 
@@ -628,15 +633,16 @@ class PagedLayer:
         return self.k_pool.shape[2]
 
     def struct(self) -> PagedLayerStruct:
-        n_sink = 0 if self.sink_block_ids is None else self.sink_block_ids.numel()
-        kd = _sk_dtype(self.k_pool.dtype)
-        return PagedLayerStruct(kd, kd if self.v_pool is None else _sk_dtype(self.v_pool.dtype), self.batch,
-                                self.n_kv_heads, _row_head_dim(self.k_pool), self.block_size,
-                                self.block_table.shape[1],
-                                n_sink, self.sinks, self.window, self.k_pool.shape[0], self.k_pool.data_ptr(),
-                                None if self.v_pool is None else self.v_pool.data_ptr(), self.block_table.data_ptr(),
-                                None if self.sink_block_ids is None else self.sink_block_ids.data_ptr(),
-                                self.seq_lens.data_ptr(), self.err.data_ptr())
+        k, v, table, sinks = self.k_pool, self.v_pool, self.block_table, self.sink_block_ids
+        kd = _sk_dtype(k.dtype)
+        n_blocks, H, bs, D = k.shape
+        B, max_blocks = table.shape
+        return PagedLayerStruct(kd, kd if v is None else _sk_dtype(v.dtype), B, H,
+                                _kv4_head_dim(D) if kd == SK_I4 else D, bs, max_blocks,
+                                0 if sinks is None else sinks.numel(), self.sinks, self.window, n_blocks,
+                                k.data_ptr(), None if v is None else v.data_ptr(), table.data_ptr(),
+                                None if sinks is None else sinks.data_ptr(), self.seq_lens.data_ptr(),
+                                self.err.data_ptr())
 
     def error_bits(self) -> int:
         return int(self.err.item())
@@ -667,16 +673,17 @@ def paged_decode_attention(layer: PagedLayer, q_rot: torch.Tensor, out: Optional
     Hq = q_rot.shape[1]
     if out is None:
         out = torch.empty_like(q_rot)
-    s = layer.struct()
-    need = int(_lib().sk_paged_decode_workspace_bytes(ctypes.byref(s), Hq))
+    lib, s = _lib(), layer.struct()
+    ref = ctypes.byref(s)
+    need = lib.sk_paged_decode_workspace_bytes(ref, Hq)
     if need == 0:
         raise SinkKVError(SK_ERR_UNSUPPORTED, "sk_paged_decode_workspace_bytes")
-    if workspace is None or workspace.numel() * workspace.element_size() < need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q_rot.device)
-    _check(_lib().sk_paged_decode_attention(ctypes.byref(s), _ptr(q_rot), Hq, _sk_dtype(q_rot.dtype),
-                                            _sink_logits(sink_logits, Hq), _ptr(out), _ptr(workspace),
-                                            workspace.numel() * workspace.element_size(), _stream(stream)),
-           "sk_paged_decode_attention")
+    size = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    if size < need:
+        size, workspace = need, torch.empty(need, dtype=torch.uint8, device=q_rot.device)
+    _check(lib.sk_paged_decode_attention(ref, q_rot.data_ptr(), Hq, _sk_dtype(q_rot.dtype),
+                                         _sink_logits(sink_logits, Hq), out.data_ptr(), workspace.data_ptr(), size,
+                                         _stream(stream)), "sk_paged_decode_attention")
     return out
 
 
